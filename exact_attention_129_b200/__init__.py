@@ -12,6 +12,9 @@ attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, ...)
 attn_bwd(q, k, v, out, lse, dout, cu_seqlens_q, cu_seqlens_k, ...)
     -> (dq, dk, dv)
 attention(...)  autograd-aware forward (backward through attn_bwd)
+attn_rotary(q, k, inv_freq, ...), rotary(...)  rotary positions, and with autograd
+attn_paged_append(k, v, k_cache, v_cache, ...)  rotated keys and values into a paged cache
+attn_paged_fwd(q, k_cache, v_cache, block_table, ...)  attention over a paged cache
 last_device_error() -> (status, message)
 """
 from __future__ import annotations
@@ -24,7 +27,9 @@ import torch
 __all__ = ["attn_fwd", "attn_bwd", "attention", "bwd_workspace_size", "fwd_split_workspace_size",
            "last_device_error",
            "set_timing_events", "KERNEL_FWD", "KERNEL_BWD_MAIN",
-           "library", "LIB_PATH", "AttnError", "STATUS"]
+           "library", "LIB_PATH", "AttnError", "STATUS",
+           "rope_frequencies", "attn_rotary", "rotary", "attn_paged_append", "attn_paged_fwd",
+           "paged_workspace_size"]
 
 # ATTN_LIBRARY names another build of the same library (a variant built with
 # exact_attention_129_b200.build.build(out=..., extra=...)); default: the in-tree build
@@ -35,7 +40,8 @@ STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED",
 EXPORTED = ("attn_fwd", "attn_bwd", "attn_fwd_ex", "attn_bwd_ex", "attn_fwd_split",
             "attn_fwd_split_workspace_size", "attn_bwd_workspace_size",
             "attn_last_device_error", "attn_set_timing_events", "attn_bwd_static_scratch",
-            "attn_watchdog_selftest", "attn_version")
+            "attn_watchdog_selftest", "attn_version", "attn_rotary", "attn_paged_append",
+            "attn_paged_fwd", "attn_paged_workspace_size")
 KERNEL_FWD, KERNEL_BWD_MAIN = 0, 1
 
 
@@ -89,6 +95,7 @@ def library() -> ctypes.CDLL:
         lib.attn_bwd_static_scratch.restype = ctypes.c_int
         lib.attn_watchdog_selftest.argtypes = [i32, vp]
         lib.attn_watchdog_selftest.restype = ctypes.c_int
+        serving.declare(lib)
         _lib = lib
     return _lib
 
@@ -301,3 +308,8 @@ def attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, *
     return _Attention.apply(q, k, v, cu_seqlens_q, cu_seqlens_k, int(max_seqlen_q),
                             int(max_seqlen_k), float(scale), bool(causal), window,
                             float(softcap or 0.0))
+
+
+from . import serving  # noqa: E402  (it uses the checks above)
+from .serving import (attn_paged_append, attn_paged_fwd, attn_rotary,  # noqa: E402
+                      paged_workspace_size, rope_frequencies, rotary)

@@ -14,9 +14,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libattn.so")
-SOURCES = ["api.cu"]
+SOURCES = ["api.cu", "serve_api.cu"]
 HEADERS = ["ptx.cuh", "fwd_kernel.cuh", "fwd_pair_kernel.cuh", "bwd_kernels.cuh",
-           "bwd_pair_kernel.cuh"]
+           "bwd_pair_kernel.cuh", "rotary.cuh", "paged_append.cuh", "paged_attn.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
@@ -42,7 +42,7 @@ def build(force: bool = False, verbose: bool = False, extra=(), out: str | None 
         return LIB
     tmp = target + f".tmp{os.getpid()}"
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
-           "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
+           "-std=c++17", "-t", "0", "-shared", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
            "--expt-relaxed-constexpr", "-Xptxas", "-v" if verbose else "-O3",
            *extra, *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,469 @@
+// serve_api.cu -- the C ABI of rotary positions and of the paged key/value
+// cache: argument checks, kernel choice and launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "attn.h"
+#include "paged_append.cuh"
+#include "paged_attn.cuh"
+#include "rotary.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kServeDevices = 64;
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+struct ServeDevice {
+  int major = 0, sms = 0;
+};
+
+// compute capability and SM count of the current device; null if there is none
+const ServeDevice* serve_device() {
+  static ServeDevice state[kServeDevices];
+  static bool known[kServeDevices];  // the values never change: a race rewrites the same ones
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kServeDevices) return nullptr;
+  if (!__atomic_load_n(&known[dev], __ATOMIC_ACQUIRE)) {
+    ServeDevice d;
+    if (cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return nullptr;
+    __atomic_store_n(&state[dev].major, d.major, __ATOMIC_RELAXED);
+    __atomic_store_n(&state[dev].sms, d.sms, __ATOMIC_RELAXED);
+    __atomic_store_n(&known[dev], true, __ATOMIC_RELEASE);
+  }
+  return &state[dev];
+}
+
+attn_status_t device_ready(const ServeDevice** out) {
+  const ServeDevice* d = serve_device();
+  if (!d) return ATTN_ERR_CUDA;
+  if (d->major != 10) return ATTN_ERR_UNSUPPORTED;
+  *out = d;
+  return ATTN_OK;
+}
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// strides of bf16 rows: 16-byte accesses at every head of every token
+bool row_strides(int64_t st, int64_t sh) { return st % 8 == 0 && sh % 8 == 0; }
+
+bool head_dim_ok(int32_t d) { return d == 64 || d == 128 || d == 256; }
+
+attn_status_t rope_args(const double* inv_freq, int32_t num_freqs, int32_t interleaved,
+                        float mscale, int32_t inverse, int32_t d, RopeParams* r) {
+  if (num_freqs < 0 || (num_freqs > 0 && !inv_freq)) return ATTN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0) return ATTN_ERR_INVALID_ARG;
+  if (num_freqs % 8 != 0 || 2 * static_cast<int64_t>(num_freqs) > d) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(mscale)) return ATTN_ERR_INVALID_ARG;
+  r->inv_freq = inv_freq;
+  r->half = num_freqs;
+  r->interleaved = interleaved != 0;
+  r->mscale = mscale;
+  r->sign = inverse ? -1.f : 1.f;
+  return ATTN_OK;
+}
+
+attn_status_t launched() {
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int page_shift_of(int32_t page_size) {
+  for (int s = 4; s <= 7; ++s)
+    if (page_size == (1 << s)) return s;
+  return -1;
+}
+
+// the checks that every use of a cache shares
+attn_status_t check_cache(const attn_paged_cache_t* c) {
+  if (!c || !c->k || !c->v || !c->block_table || !on16(c->k) || !on16(c->v) ||
+      !on4(c->block_table))
+    return ATTN_ERR_INVALID_ARG;
+  if (c->type != ATTN_CACHE_BF16 && c->type != ATTN_CACHE_E4M3) return ATTN_ERR_INVALID_ARG;
+  if (!head_dim_ok(c->head_dim)) return ATTN_ERR_UNSUPPORTED;
+  if (page_shift_of(c->page_size) < 0) return ATTN_ERR_UNSUPPORTED;
+  const bool e4m3 = c->type == ATTN_CACHE_E4M3;
+  if (e4m3 && (!c->k_scale || !c->v_scale || !on4(c->k_scale) || !on4(c->v_scale)))
+    return ATTN_ERR_INVALID_ARG;
+  const int64_t step = e4m3 ? 16 : 8;  // 16-byte accesses everywhere
+  for (int64_t s : {c->k_s_page, c->k_s_token, c->k_s_head, c->v_s_page, c->v_s_token,
+                    c->v_s_head})
+    if (s % step != 0) return ATTN_ERR_INVALID_ARG;
+  if (c->num_pages < 0 || c->pages_per_seq < 0 || c->nheads_kv < 1 || c->nheads_kv > 65535)
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+CacheView cache_view(const attn_paged_cache_t* c, bool v) {
+  CacheView r;
+  r.p = static_cast<uint8_t*>(v ? c->v : c->k);
+  r.scale = c->type == ATTN_CACHE_E4M3 ? (v ? c->v_scale : c->k_scale) : nullptr;
+  r.s_page = v ? c->v_s_page : c->k_s_page;
+  r.s_token = v ? c->v_s_token : c->k_s_token;
+  r.s_head = v ? c->v_s_head : c->k_s_head;
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// rotary
+// ---------------------------------------------------------------------------
+template <int D>
+attn_status_t launch_rotary(const RotaryParams& p, int64_t blocks, int groups, cudaStream_t s) {
+  attn_rotary_kernel<D><<<dim3(static_cast<unsigned>(blocks), groups), kRotaryThreads, 0, s>>>(p);
+  return launched();
+}
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+template <int D, bool E4M3>
+attn_status_t launch_append_few(const AppendParams& p, cudaStream_t s) {
+  constexpr int L = D / 16;
+  const int64_t groups = static_cast<int64_t>(p.batch) * p.page_bound * 2 * p.hkv +
+                         (p.q.p ? static_cast<int64_t>(p.total) * p.hq : 0);
+  const int64_t blocks = (groups * L + 127) / 128;
+  if (blocks > kMaxGrid) return ATTN_ERR_INVALID_ARG;
+  attn_append_few_kernel<D, E4M3><<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
+  return launched();
+}
+
+template <int D, bool E4M3, int IPT>
+attn_status_t launch_append_page_n(const AppendParams& p, int items, dim3 grid, cudaStream_t s) {
+  attn_append_page_kernel<D, E4M3, IPT><<<grid, items / IPT, 0, s>>>(p);
+  return launched();
+}
+
+template <int D, bool E4M3>
+attn_status_t launch_append_page(AppendParams p, int sms, cudaStream_t s) {
+  const int64_t units = static_cast<int64_t>(p.batch) * p.page_bound;
+  if (units > kMaxGrid) return ATTN_ERR_INVALID_ARG;
+  // a CTA walks over as many heads as leaves about four CTAs for every SM: the
+  // cosines and sines are then computed once for all of them
+  auto per_cta = [&](int heads) {
+    int64_t groups = (4ll * sms + units - 1) / units;
+    groups = std::min<int64_t>(std::max<int64_t>(groups, (heads + 7) / 8), heads);
+    return static_cast<int>((heads + groups - 1) / groups);
+  };
+  p.heads_per_cta = per_cta(p.hkv);
+  p.kv_groups = (p.hkv + p.heads_per_cta - 1) / p.heads_per_cta;
+  p.q_heads_per_cta = p.q.p ? per_cta(p.hq) : 1;
+  const int q_groups = p.q.p ? (p.hq + p.q_heads_per_cta - 1) / p.q_heads_per_cta : 0;
+  if (p.kv_groups + q_groups > 65535) return ATTN_ERR_INVALID_ARG;
+  const dim3 grid(static_cast<unsigned>(units), p.kv_groups + q_groups);
+  const int items = (D / 16) << p.page_shift;  // 64 .. 2048
+  if (items <= 512) return launch_append_page_n<D, E4M3, 1>(p, items, grid, s);
+  if constexpr (D >= 128)
+    if (items == 1024) return launch_append_page_n<D, E4M3, 2>(p, items, grid, s);
+  if constexpr (D == 256)
+    if (items == 2048) return launch_append_page_n<D, E4M3, 4>(p, items, grid, s);
+  return ATTN_ERR_UNSUPPORTED;
+}
+
+template <int D>
+attn_status_t launch_append(const AppendParams& p, bool e4m3, int max_seqlen, int sms,
+                            cudaStream_t s) {
+  if (max_seqlen <= kAppendFew)
+    return e4m3 ? launch_append_few<D, true>(p, s) : launch_append_few<D, false>(p, s);
+  return e4m3 ? launch_append_page<D, true>(p, sms, s) : launch_append_page<D, false>(p, sms, s);
+}
+
+// ---------------------------------------------------------------------------
+// attention over the cache
+// ---------------------------------------------------------------------------
+constexpr int kPagedMaxSplits = 128;
+
+// how a call is cut into CTAs; a pure function of the arguments and the device
+struct PagedPlan {
+  int nt, wr;          // query rows per CTA: 8 nt wr
+  int row_tiles;
+  int splits, chunk;   // parts of the keys, and their length
+  size_t lse_off, bytes;  // workspace: partial O, then partial LSE
+};
+
+// requested splits 0: enough parts for about two rounds of CTAs, of at least 256 keys
+PagedPlan paged_plan(const attn_paged_cache_t* c, int batch, int total_q, int max_q, int max_k,
+                     int hq, int hi_off, int lo_off, int want, int sms) {
+  PagedPlan pl;
+  const int64_t group = hq / c->nheads_kv;
+  const int64_t rows = group * max_q;
+  pl.nt = rows <= 8 ? 1 : 2;
+  pl.wr = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  const int rt = 8 * pl.nt * pl.wr;
+  pl.row_tiles = static_cast<int>((rows + rt - 1) / rt);
+  // keys a CTA's rows can see: with both bounds, the window and the rows' spread
+  int64_t span = max_k;
+  if (lo_off < kPagedNoBound && hi_off < kPagedNoBound)
+    span = std::min<int64_t>(span, static_cast<int64_t>(lo_off) + hi_off + 1 +
+                                       (rt + group - 1) / group + 1);
+  if (lo_off < kPagedNoBound) span += 15;  // parts begin at a multiple of 16
+  span = std::max<int64_t>(span, 1);
+  const int bk = (c->type == ATTN_CACHE_E4M3 && c->head_dim == 64) ? 128 : 64;
+  const int64_t ctas = static_cast<int64_t>(batch) * c->nheads_kv * pl.row_tiles;
+  int64_t splits = want;
+  if (want == 0) {
+    splits = (4ll * sms + ctas - 1) / ctas;
+    splits = std::min<int64_t>(splits, (span + 255) / 256);
+  }
+  splits = std::max<int64_t>(1, std::min<int64_t>(splits, kPagedMaxSplits));
+  int64_t chunk = (span + splits - 1) / splits;
+  chunk = (chunk + bk - 1) / bk * bk;
+  pl.splits = static_cast<int>((span + chunk - 1) / chunk);
+  pl.chunk = static_cast<int>(chunk);
+  const size_t rows_all = static_cast<size_t>(pl.splits) * total_q * hq;
+  pl.lse_off = (rows_all * c->head_dim * 4 + 255) / 256 * 256;
+  pl.bytes = pl.splits > 1 ? pl.lse_off + rows_all * 4 : 0;
+  return pl;
+}
+
+struct PagedMask {
+  int hi_off, lo_off;
+};
+PagedMask paged_mask(int32_t causal, int32_t wl, int32_t wr) {
+  PagedMask m;
+  m.hi_off = causal ? 0 : (wr >= 0 ? std::min(wr, kPagedNoBound) : kPagedNoBound);
+  m.lo_off = wl >= 0 ? std::min(wl, kPagedNoBound) : kPagedNoBound;
+  return m;
+}
+
+attn_status_t paged_sizes(const attn_paged_cache_t* c, int32_t batch, int32_t total_q,
+                          int32_t max_q, int32_t max_k, int32_t hq, int32_t num_splits) {
+  attn_status_t st = check_cache(c);
+  if (st != ATTN_OK) return st;
+  if (batch < 1 || total_q < 0 || max_q < 0 || max_k < 0 || max_k > (1 << 29) || hq < 1 ||
+      hq > 65535 || hq % c->nheads_kv != 0 || num_splits < 0 || num_splits > kPagedMaxSplits)
+    return ATTN_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(total_q) * hq * c->head_dim >= (int64_t(1) << 40))
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+template <int D, bool FP8, int NT, int WR>
+attn_status_t launch_paged(const PagedParams& p, int batch, cudaStream_t s) {
+  using C = PagedCfg<D, FP8, NT, WR>;
+  static bool ready[kServeDevices];  // the limit has been raised on this device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
+    if (cudaFuncSetAttribute(attn_paged_kernel<D, FP8, NT, WR>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    __atomic_store_n(&ready[dev], true, __ATOMIC_RELEASE);
+  }
+  const int64_t ctas = static_cast<int64_t>(batch) * p.num_splits * p.row_tiles * p.hkv;
+  if (ctas > kMaxGrid) return ATTN_ERR_INVALID_ARG;
+  attn_paged_kernel<D, FP8, NT, WR><<<static_cast<unsigned>(ctas), 128, C::SMEM, s>>>(p);
+  attn_status_t st = launched();
+  if (st != ATTN_OK || p.num_splits == 1) return st;
+  const int64_t warps = static_cast<int64_t>(p.total_q) * p.hq;
+  attn_paged_merge_kernel<D><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, s>>>(p, batch);
+  return launched();
+}
+
+template <int D, bool FP8>
+attn_status_t launch_paged_rows(const PagedParams& p, const PagedPlan& pl, int batch,
+                                cudaStream_t s) {
+  if (pl.nt == 1) return launch_paged<D, FP8, 1, 1>(p, batch, s);
+  if (pl.wr == 1) return launch_paged<D, FP8, 2, 1>(p, batch, s);
+  if (pl.wr == 2) return launch_paged<D, FP8, 2, 2>(p, batch, s);
+  return launch_paged<D, FP8, 2, 4>(p, batch, s);
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" attn_status_t attn_rotary(
+    const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st, int64_t k_sh,
+    void* q_out, int64_t qo_st, int64_t qo_sh, void* k_out, int64_t ko_st, int64_t ko_sh,
+    const double* inv_freq, int32_t num_freqs, int32_t interleaved, float mscale, int32_t inverse,
+    const int32_t* positions, const int32_t* cu_seqlens, const int32_t* offsets, int32_t batch,
+    int32_t zero_outside, int32_t total, int32_t nheads_q, int32_t nheads_kv, int32_t head_dim,
+    attn_stream_t stream) {
+  RotaryParams p;
+  if (!q || !q_out || (k == nullptr) != (k_out == nullptr) || !on16(q) || !on16(q_out) ||
+      !on16(k) || !on16(k_out))
+    return ATTN_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim)) return ATTN_ERR_UNSUPPORTED;
+  if (!row_strides(q_st, q_sh) || !row_strides(qo_st, qo_sh) || !row_strides(k_st, k_sh) ||
+      !row_strides(ko_st, ko_sh))
+    return ATTN_ERR_INVALID_ARG;
+  if (total < 0 || nheads_q < 1 || nheads_kv < 0 || (k ? nheads_kv < 1 : nheads_kv != 0) ||
+      nheads_q > 65535 || nheads_kv > 65535)
+    return ATTN_ERR_INVALID_ARG;
+  if (!on4(positions) || !on4(cu_seqlens) || !on4(offsets) || (cu_seqlens && batch < 1) ||
+      (offsets && !cu_seqlens) || (positions && cu_seqlens))
+    return ATTN_ERR_INVALID_ARG;
+  attn_status_t st = rope_args(inv_freq, num_freqs, interleaved, mscale, inverse, head_dim, &p.rope);
+  if (st != ATTN_OK) return st;
+  const ServeDevice* dev = nullptr;
+  if ((st = device_ready(&dev)) != ATTN_OK) return st;
+  if (total == 0) return ATTN_OK;
+  p.q = {static_cast<const uint16_t*>(q), q_st, q_sh};
+  p.k = {static_cast<const uint16_t*>(k), k_st, k_sh};
+  p.qo = {static_cast<uint16_t*>(q_out), qo_st, qo_sh};
+  p.ko = {static_cast<uint16_t*>(k_out), ko_st, ko_sh};
+  p.positions = positions;
+  p.cu = cu_seqlens;
+  p.offsets = offsets;
+  p.zero_outside = zero_outside != 0;
+  p.batch = batch;
+  p.total = total;
+  p.hq = nheads_q;
+  p.heads = nheads_q + nheads_kv;
+  const int64_t blocks =
+      (static_cast<int64_t>(total) * (head_dim / 16) + kRotaryThreads - 1) / kRotaryThreads;
+  if (blocks > kMaxGrid) return ATTN_ERR_INVALID_ARG;
+  // heads per thread: 8 (the angles' cost is then spread over 8 heads) where
+  // that still gives every SM 8 blocks, fewer down to 1 for few tokens
+  const int64_t want = std::max<int64_t>(1, (8ll * dev->sms + blocks - 1) / blocks);
+  p.heads_per_thread = static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>(8, p.heads / std::min<int64_t>(want, p.heads))));
+  const int groups = (p.heads + p.heads_per_thread - 1) / p.heads_per_thread;
+  if (groups > 65535) return ATTN_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (head_dim) {
+    case 64: return launch_rotary<64>(p, blocks, groups, s);
+    case 128: return launch_rotary<128>(p, blocks, groups, s);
+    default: return launch_rotary<256>(p, blocks, groups, s);
+  }
+}
+
+extern "C" attn_status_t attn_paged_append(
+    const attn_paged_cache_t* cache, const void* k, int64_t k_st, int64_t k_sh, const void* v,
+    int64_t v_st, int64_t v_sh, const void* q, int64_t q_st, int64_t q_sh, void* q_out,
+    int64_t qo_st, int64_t qo_sh, const int32_t* cu_seqlens, const int32_t* seqlens_k,
+    int32_t batch, int32_t total, int32_t max_seqlen, int32_t nheads_q, const double* inv_freq,
+    int32_t num_freqs, int32_t interleaved, float mscale, attn_stream_t stream) {
+  attn_status_t st = check_cache(cache);
+  if (st != ATTN_OK) return st;
+  if (!k || !v || !on16(k) || !on16(v) || (q == nullptr) != (q_out == nullptr) || !on16(q) ||
+      !on16(q_out))
+    return ATTN_ERR_INVALID_ARG;
+  if (!row_strides(k_st, k_sh) || !row_strides(v_st, v_sh) || !row_strides(q_st, q_sh) ||
+      !row_strides(qo_st, qo_sh))
+    return ATTN_ERR_INVALID_ARG;
+  if (!cu_seqlens || !seqlens_k || !on4(cu_seqlens) || !on4(seqlens_k) || batch < 1 ||
+      total < 0 || max_seqlen < 0 || nheads_q < 0 || (q ? nheads_q < 1 : nheads_q != 0) ||
+      nheads_q > 65535)
+    return ATTN_ERR_INVALID_ARG;
+  AppendParams p;
+  st = rope_args(inv_freq, num_freqs, interleaved, mscale, 0, cache->head_dim, &p.rope);
+  if (st != ATTN_OK) return st;
+  const ServeDevice* dev = nullptr;
+  if ((st = device_ready(&dev)) != ATTN_OK) return st;
+  max_seqlen = std::min(max_seqlen, total);
+  if (max_seqlen == 0) return ATTN_OK;
+  p.k = {static_cast<const uint16_t*>(k), k_st, k_sh};
+  p.v = {static_cast<const uint16_t*>(v), v_st, v_sh};
+  p.q = {static_cast<const uint16_t*>(q), q_st, q_sh};
+  p.qo = {static_cast<uint16_t*>(q_out), qo_st, qo_sh};
+  p.kc = cache_view(cache, false);
+  p.vc = cache_view(cache, true);
+  p.table = cache->block_table;
+  p.table_stride = cache->table_stride;
+  p.cu = cu_seqlens;
+  p.seqlens = seqlens_k;
+  p.batch = batch;
+  p.total = total;
+  p.hq = nheads_q;
+  p.hkv = cache->nheads_kv;
+  p.page_shift = page_shift_of(cache->page_size);
+  p.num_pages = cache->num_pages;
+  p.pages_per_seq = cache->pages_per_seq;
+  p.page_bound = static_cast<int>(
+      (static_cast<int64_t>(max_seqlen) + cache->page_size - 2) / cache->page_size + 1);
+  const bool e4m3 = cache->type == ATTN_CACHE_E4M3;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (cache->head_dim) {
+    case 64: return launch_append<64>(p, e4m3, max_seqlen, dev->sms, s);
+    case 128: return launch_append<128>(p, e4m3, max_seqlen, dev->sms, s);
+    default: return launch_append<256>(p, e4m3, max_seqlen, dev->sms, s);
+  }
+}
+
+extern "C" size_t attn_paged_workspace_size(const attn_paged_cache_t* cache, int32_t batch,
+                                            int32_t total_q, int32_t max_seqlen_q,
+                                            int32_t max_seqlen_k, int32_t nheads_q, int32_t causal,
+                                            int32_t window_left, int32_t window_right,
+                                            int32_t num_splits) {
+  if (paged_sizes(cache, batch, total_q, max_seqlen_q, max_seqlen_k, nheads_q, num_splits) !=
+      ATTN_OK)
+    return 0;
+  const ServeDevice* dev = serve_device();
+  if (!dev || total_q == 0 || max_seqlen_q == 0) return 0;
+  const PagedMask m = paged_mask(causal, window_left, window_right);
+  return paged_plan(cache, batch, total_q, std::min(max_seqlen_q, total_q), max_seqlen_k, nheads_q,
+                    m.hi_off, m.lo_off, num_splits, dev->sms)
+      .bytes;
+}
+
+extern "C" attn_status_t attn_paged_fwd(
+    const attn_paged_cache_t* cache, const void* q, const int32_t* cu_seqlens_q,
+    const int32_t* seqlens_k, int32_t batch, int32_t total_q, int32_t max_seqlen_q,
+    int32_t max_seqlen_k, int32_t nheads_q, float scale, int32_t causal, int32_t window_left,
+    int32_t window_right, float softcap, int32_t num_splits, int32_t return_lse, void* out,
+    float* lse, void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  attn_status_t st = paged_sizes(cache, batch, total_q, max_seqlen_q, max_seqlen_k, nheads_q,
+                                 num_splits);
+  if (st != ATTN_OK) return st;
+  if (!q || !on16(q) || !out || !on16(out) || !cu_seqlens_q || !seqlens_k ||
+      !on4(cu_seqlens_q) || !on4(seqlens_k) || (return_lse && (!lse || !on4(lse))))
+    return ATTN_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f) || !std::isfinite(softcap) || softcap < 0.f)
+    return ATTN_ERR_INVALID_ARG;
+  const ServeDevice* dev = nullptr;
+  if ((st = device_ready(&dev)) != ATTN_OK) return st;
+  if (total_q == 0 || max_seqlen_q == 0) return ATTN_OK;
+  const PagedMask m = paged_mask(causal, window_left, window_right);
+  const PagedPlan pl = paged_plan(cache, batch, total_q, std::min(max_seqlen_q, total_q),
+                                  max_seqlen_k, nheads_q, m.hi_off, m.lo_off, num_splits, dev->sms);
+  if (pl.bytes > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+                       workspace_bytes < pl.bytes))
+    return ATTN_ERR_INVALID_ARG;
+  PagedParams p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.kc = cache_view(cache, false);
+  p.vc = cache_view(cache, true);
+  p.table = cache->block_table;
+  p.table_stride = cache->table_stride;
+  p.cu = cu_seqlens_q;
+  p.seqlens = seqlens_k;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = return_lse ? lse : nullptr;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = pl.bytes ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.lse_off)
+                        : nullptr;
+  p.total_q = total_q;
+  p.hq = nheads_q;
+  p.hkv = cache->nheads_kv;
+  p.group = nheads_q / cache->nheads_kv;
+  p.page_shift = page_shift_of(cache->page_size);
+  p.num_pages = cache->num_pages;
+  p.pages_per_seq = cache->pages_per_seq;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.cap_mul = softcap > 0.f ? 2.f / softcap : 0.f;
+  p.cap_log2 = softcap * 1.4426950408889634f;
+  p.hi_off = m.hi_off;
+  p.lo_off = m.lo_off;
+  p.num_splits = pl.splits;
+  p.chunk = pl.chunk;
+  p.row_tiles = pl.row_tiles;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->type == ATTN_CACHE_E4M3;
+  switch (cache->head_dim) {
+    case 64:
+      return e4m3 ? launch_paged_rows<64, true>(p, pl, batch, s)
+                  : launch_paged_rows<64, false>(p, pl, batch, s);
+    case 128:
+      return e4m3 ? launch_paged_rows<128, true>(p, pl, batch, s)
+                  : launch_paged_rows<128, false>(p, pl, batch, s);
+    default:
+      return e4m3 ? launch_paged_rows<256, true>(p, pl, batch, s)
+                  : launch_paged_rows<256, false>(p, pl, batch, s);
+  }
+}

@@ -266,6 +266,166 @@ attn_status_t attn_bwd_static_scratch(const void* q, const void* k, const void* 
                                       float scale, int32_t causal,
                                       void* dq, void* dk, void* dv, attn_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions, and serving from a paged key/value cache
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Rotary position embedding of packed rows: q and, unless k is NULL, k.
+ *
+ * With R = 2 * num_freqs, pair i < num_freqs of a row at position pos is
+ * (x[i], x[i + R/2]), or (x[2i], x[2i+1]) when interleaved, and becomes, for
+ * theta = pos * inv_freq[i] (computed in 64 bits),
+ *   a' = mscale (a cos theta - b sin theta), b' = mscale (b cos theta + a sin theta);
+ * elements from R on are copied.  inverse = 1 turns by -theta: the gradient of
+ * the forward rotation with respect to its input, given the output's.
+ *
+ *   q, k           bf16 [total][nheads][head_dim]; the last dimension is
+ *                  contiguous, *_st and *_sh are the strides of tokens and
+ *                  heads in elements, multiples of 8.
+ *   q_out, k_out   written, with strides of their own; they may be q and k
+ *                  themselves (the same pointer and strides) but must not
+ *                  overlap them in any other way.
+ *   inv_freq       device fp64 [num_freqs]; 2 * num_freqs is a multiple of 16
+ *                  and at most head_dim (64, 128 or 256).
+ *   positions      device int32 [total], or NULL: then
+ *   cu_seqlens     device int32 [batch + 1], or NULL, gives row t of segment b
+ *                  the position t - cu_seqlens[b] + offsets[b], with
+ *   offsets        device int32 [batch], or NULL for zeros.  Rows outside
+ *                  [cu_seqlens[0], cu_seqlens[batch]) are left as they were in
+ *                  the outputs, or with zero_outside written as zeros.
+ *                  Without positions and cu_seqlens the position is the row.
+ * nheads_kv is 0 when k is NULL.  Every pointer to rows is 16-byte aligned.
+ */
+attn_status_t attn_rotary(const void* q, int64_t q_st, int64_t q_sh, const void* k, int64_t k_st,
+                          int64_t k_sh, void* q_out, int64_t qo_st, int64_t qo_sh, void* k_out,
+                          int64_t ko_st, int64_t ko_sh, const double* inv_freq, int32_t num_freqs,
+                          int32_t interleaved, float mscale, int32_t inverse,
+                          const int32_t* positions, const int32_t* cu_seqlens,
+                          const int32_t* offsets, int32_t batch, int32_t zero_outside,
+                          int32_t total, int32_t nheads_q, int32_t nheads_kv, int32_t head_dim,
+                          attn_stream_t stream);
+
+/*
+ * A paged key/value cache: a pool of pages of page_size tokens, and a block
+ * table that names each sequence's pages in order.
+ *
+ *   k, v         element (page, token of the page, head, d) is at
+ *                page * s_page + token * s_token + head * s_head + d; the
+ *                strides are in elements, their bytes multiples of 16, the
+ *                pointers 16-byte aligned.  Any order of the three outer
+ *                dimensions serves; heads before tokens keeps a page's rows of
+ *                one head together, which the attention reads a little faster.
+ *   type         ATTN_CACHE_BF16, or ATTN_CACHE_E4M3: 8-bit floats whose value
+ *                is the code times the scale of its page and head.
+ *   k_scale,     fp32 [num_pages][nheads_kv], > 0 (e4m3; NULL for bf16).  Value
+ *   v_scale      scales from 2^-64 to 2^64 keep the attention's accuracy.
+ *   block_table  int32, row b at block_table + b * table_stride holds
+ *                pages_per_seq page numbers; token p of sequence b is in page
+ *                row[p / page_size].  Entries past a sequence's length are not
+ *                read.  A number outside [0, num_pages) is never followed: such
+ *                tokens are not written, and read as zeros.
+ *   page_size    16, 32, 64 or 128.
+ */
+enum { ATTN_CACHE_BF16 = 0, ATTN_CACHE_E4M3 = 1 };
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  int64_t k_s_page, k_s_token, k_s_head;
+  int64_t v_s_page, v_s_token, v_s_head;
+  int64_t table_stride;
+  int32_t type;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t pages_per_seq;
+  int32_t nheads_kv;
+  int32_t head_dim;
+} attn_paged_cache_t;
+
+/*
+ * Appends new keys and values to a paged cache, the keys rotated on the way,
+ * and rotates the queries of the same tokens in the same launch.
+ *
+ *   cache          described above; its pages and scales are written.
+ *   k, v           bf16 [total][nheads_kv][head_dim], strides as in attn_rotary.
+ *   q, q_out       bf16 [total][nheads_q][head_dim], or both NULL; q_out may be
+ *                  q itself.  q is not written to the cache.
+ *   cu_seqlens     int32 [batch + 1]: sequence b's new tokens are the packed
+ *                  rows [cu_seqlens[b], cu_seqlens[b+1]); may be none.
+ *   seqlens_k      int32 [batch]: tokens of each sequence, the new ones
+ *                  included, so new token i of n has position
+ *                  seqlens_k[b] - n + i.
+ *   max_seqlen     upper bound of the new tokens of any sequence.
+ *   inv_freq, num_freqs, interleaved, mscale   as in attn_rotary; inv_freq NULL
+ *                  (num_freqs 0): nothing is rotated.
+ *
+ * A bf16 cache gets the bits that attn_rotary would write.  In an e4m3 cache
+ * the bf16 row y is stored as codes y / s, rounded to nearest even, under the
+ * scale s of its page and head.  This call's tokens in a page need the least
+ * power of two >= 2^-64 that makes max |y| <= 448 s (over finite y); s becomes
+ * that where the call writes the page's first slot, and the larger of it and
+ * the old scale elsewhere.  Where a scale grows, the codes already in the page
+ * are moved to it (exactly, for powers of two, down to the smallest normal
+ * code).  Infinities and NaN are held as NaN.
+ * Two sequences of one call must not append to the same page.  Rows behind
+ * cu_seqlens[batch] are not read, and q_out is left as it was there.
+ */
+attn_status_t attn_paged_append(const attn_paged_cache_t* cache, const void* k, int64_t k_st,
+                                int64_t k_sh, const void* v, int64_t v_st, int64_t v_sh,
+                                const void* q, int64_t q_st, int64_t q_sh, void* q_out,
+                                int64_t qo_st, int64_t qo_sh, const int32_t* cu_seqlens,
+                                const int32_t* seqlens_k, int32_t batch, int32_t total,
+                                int32_t max_seqlen, int32_t nheads_q, const double* inv_freq,
+                                int32_t num_freqs, int32_t interleaved, float mscale,
+                                attn_stream_t stream);
+
+/*
+ * Attention of new query rows over a paged cache: the forward of attn_fwd_ex
+ * with keys and values read from the pages (e4m3: times their page's scales).
+ *
+ *   q              bf16 [total_q][nheads_q][head_dim], contiguous; query head h
+ *                  reads key/value head h / (nheads_q / cache->nheads_kv).
+ *   cu_seqlens_q   int32 [batch + 1], as in attn_fwd: one row per sequence when
+ *                  decoding, a few when verifying drafts, many for the chunk of
+ *                  a prompt; a sequence may have none.
+ *   seqlens_k      int32 [batch], keys of each sequence, 0 or more.  With causal
+ *                  or window the rows are its last ones (bottom-right).
+ *   max_seqlen_q/k upper bounds of those lengths; they choose the kernel and the
+ *                  split, and seqlens_k beyond pages_per_seq * page_size are
+ *                  cut off there.
+ *   scale, causal, window_left, window_right, softcap, return_lse, out, lse
+ *                  as in attn_fwd_ex.  A row with no allowed key gets O = 0 and
+ *                  LSE = -inf; rows behind cu_seqlens_q[batch] are left as they
+ *                  were.
+ *   num_splits     parts each sequence's keys are cut into, 1..128, merged by a
+ *                  second kernel; 0: the library's choice.
+ *   workspace      device memory of at least attn_paged_workspace_size(...)
+ *                  bytes for the same arguments, 256-byte aligned, clobbered;
+ *                  NULL when that is 0.  Calls sharing it must not overlap on
+ *                  the GPU.
+ * What the slots of a page past the sequence's length hold, and the pages of
+ * other sequences, NaN included, never reaches the result.
+ */
+attn_status_t attn_paged_fwd(const attn_paged_cache_t* cache, const void* q,
+                             const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int32_t batch,
+                             int32_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                             int32_t nheads_q, float scale, int32_t causal, int32_t window_left,
+                             int32_t window_right, float softcap, int32_t num_splits,
+                             int32_t return_lse, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * Bytes of workspace attn_paged_fwd needs for these arguments on the current
+ * device (0: none, or the arguments are not valid).
+ */
+size_t attn_paged_workspace_size(const attn_paged_cache_t* cache, int32_t batch, int32_t total_q,
+                                 int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t nheads_q,
+                                 int32_t causal, int32_t window_left, int32_t window_right,
+                                 int32_t num_splits);
+
 /*
  * Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns ATTN_OK, ATTN_ERR_TIMEOUT (a bounded wait in a kernel ran out;

@@ -1,0 +1,451 @@
+"""Appending to a paged cache and attention over it, on the GPU, against the
+64-bit definitions."""
+import math
+
+import pytest
+import torch
+
+import exact_attention_129_b200 as ea
+from tests import serving_ref as sr
+from tests.gpu_helpers import LSE_TOL, guarded_empty, guards_intact
+from tests.serving_ref import Cache
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def rows(t, h, d, seed, spread=0.5):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(t, h, d, generator=g) * torch.exp(spread * torch.randn(t, h, 1, generator=g))
+    return x.to(BF)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+def cu_of(n):
+    cu = [0]
+    for x in n:
+        cu.append(cu[-1] + x)
+    return cu
+
+
+def bits(x):
+    return x.view(torch.uint8 if x.dtype == sr.E4M3 else torch.int16)
+
+
+def same_codes(a, b):
+    """Equal bit for bit, any NaN alike."""
+    x, y = bits(a.contiguous()), bits(b.contiguous())
+    nan = a.float().isnan().reshape(x.shape) & b.float().isnan().reshape(y.shape)
+    return bool(((x == y) | nan).all())
+
+
+# ---------------------------------------------------------------------------
+# append
+# ---------------------------------------------------------------------------
+APPENDS = [  # new tokens, tokens before them
+    ([1], [0]), ([1, 1, 1], [0, 15, 16]), ([3, 0, 8, 1], [14, 5, 120, 0]),
+    ([9, 40], [0, 7]), ([200, 1, 0, 129], [30, 300, 2, 127]),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append(d, page, e4m3):
+    hkv = 3
+    for n, before in APPENDS:
+        for head_major in (True, False):
+            lens, cu = [a + b for a, b in zip(n, before)], cu_of(n)
+            c = Cache(before, lens, hkv, d, page, e4m3, head_major, seed=len(n), spread=1.5)
+            k, v = rows(cu[-1], hkv, d, 1), rows(cu[-1], hkv, d, 2)
+            kc, vc, table, kw = c.to("cuda")
+            ea.attn_paged_append(k.cuda(), v.cuda(), kc, vc, table, i32(cu), i32(lens), max(n),
+                                 **kw)
+            for x, pool, got, name in ((k, c.k, kc, "k"), (v, c.v, vc, "v")):
+                scale = getattr(c, name + "_scale")
+                sr.append(x, pool, scale, c.table, cu, lens)
+                assert same_codes(got.cpu(), pool), (n, before, head_major, name)
+                if e4m3:
+                    assert torch.equal(kw[name + "_scale"].cpu(), scale)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d,rot,inter", [(64, 32, False), (128, 128, False), (128, 80, True),
+                                         (256, 256, True), (256, 64, False)])
+def test_append_rotates_as_rotary_does(e4m3, d, rot, inter):
+    hq, hkv, page = 6, 2, 32
+    f, m = ea.rope_frequencies(rot, scaling="yarn", factor=8, original_max=4096)
+    for n, before in (([3, 1, 0, 8], [40, 0, 9, 100000]), ([90, 5, 33], [0, 61, 100])):
+        lens, cu = [a + b for a, b in zip(n, before)], cu_of(n)
+        q, k, v = (rows(cu[-1], h, d, s).cuda() for s, h in enumerate((hq, hkv, hkv)))
+        c = Cache([0] * len(n), [min(x, 200) for x in lens], hkv, d, page, e4m3, seed=7)
+        # far positions share few pages: the table names them at the end of its row
+        width = -(-max(lens) // page)
+        table = torch.full((len(n), width), -1, dtype=torch.int32)
+        for b, (x, y) in enumerate(zip(before, lens)):
+            for j in range(x // page, -(-y // page)):
+                table[b, j] = c.table[b, j - x // page]
+        kc, vc, _, kw = c.to("cuda")
+        kc2, vc2, _, kw2 = c.to("cuda")
+        args = (table.cuda(), i32(cu), i32(lens), max(n))
+        qo = ea.attn_paged_append(k, v, kc, vc, *args, q=q, inv_freq=f.cuda(), interleaved=inter,
+                                  mscale=m, **kw)
+        qr, kr = ea.attn_rotary(q, k, f.cuda(), cu_seqlens=i32(cu), offsets=i32(before),
+                                interleaved=inter, mscale=m)
+        assert torch.equal(qo, qr)
+        ea.attn_paged_append(kr, v, kc2, vc2, *args, **kw2)
+        assert same_codes(kc, kc2) and same_codes(vc, vc2)
+        for name in kw:
+            assert torch.equal(kw[name], kw2[name])
+
+
+def test_append_holds_what_is_not_finite_as_nan():
+    d, page = 64, 16
+    k = rows(4, 2, d, 3)
+    k[0, 0, 5], k[1, 1, 7], k[2, 0, 9], k[3, 1] = math.inf, math.nan, -math.inf, 0.0
+    for n in ([4], [2, 2]):  # both kernels: 4 tokens of one page, then padded to many
+        cu, before = cu_of(n), [6] * len(n)
+        lens = [a + b for a, b in zip(n, before)]
+        c = Cache(before, lens, 2, d, page, True, seed=3, spread=3.0)
+        for max_n in (max(n), 40):
+            kc, vc, table, kw = c.to("cuda")
+            ea.attn_paged_append(k.cuda(), k.cuda(), kc, vc, table, i32(cu), i32(lens), max_n, **kw)
+            ref, scale = c.k.clone(), c.k_scale.clone()
+            sr.append(k, ref, scale, c.table, cu, lens)
+            assert same_codes(kc.cpu(), ref) and torch.equal(kw["k_scale"].cpu(), scale)
+            assert bool(torch.isfinite(kw["k_scale"]).all())
+
+
+@pytest.mark.parametrize("max_n", [8, 64])
+def test_append_leaves_the_rest_alone(max_n):
+    # pages of nobody, slots behind the tokens, rows behind the last sequence, table
+    # entries outside the pool and positions outside the table
+    d, page, hkv = 64, 16, 2
+    c = Cache([20, 3], [40, 16], hkv, d, page, True, seed=5)
+    c.table[0, 1] = 10 ** 6     # tokens 16 .. 31 of sequence 0 go nowhere
+    n, lens = [7, 5], [27, 20]  # sequence 1: tokens 15 .. 19, its row has 1 usable page + -7s
+    cu = [0, 7, 12]
+    k, q = rows(15, hkv, d, 6).cuda(), rows(15, 4, d, 7).cuda()
+    kc, vc, table, kw = c.to("cuda")
+    out = torch.full_like(q, 3.0)
+    f = ea.rope_frequencies(d)[0].cuda()
+    ea.attn_paged_append(k, k, kc, vc, table, i32(cu), i32(lens), max_n, q=q, q_out=out, inv_freq=f,
+                         **kw)
+    kr = ea.attn_rotary(k[:12], None, f, cu_seqlens=i32(cu), offsets=i32([20, 15]))[0]
+    for x, pool, got, name in ((kr.cpu(), c.k, kc, "k"), (k.cpu(), c.v, vc, "v")):
+        scale = getattr(c, name + "_scale")
+        sr.append(x, pool, scale, c.table, cu, lens)
+        assert same_codes(got.cpu(), pool) and torch.equal(kw[name + "_scale"].cpu(), scale)
+    assert bool((out[12:] == 3).all())
+    assert torch.equal(out[:12], ea.attn_rotary(q[:12], None, f, cu_seqlens=i32(cu),
+                                                offsets=i32([20, 15]))[0])
+
+
+def test_append_views_and_queries_in_place():
+    d, page = 128, 64
+    n, before = [5, 1], [61, 0]
+    cu, lens = cu_of(n), [66, 1]
+    qkv = rows(6, 8, d, 8)
+    f = ea.rope_frequencies(d)[0].cuda()
+    c = Cache(before, lens, 2, d, page, True)
+    for max_n in (5, 100):
+        a, b = c.to("cuda"), c.to("cuda")
+        dev = qkv.cuda()
+        q, k, v = dev[:, :4], dev[:, 4:6], dev[:, 6:]
+        want = ea.attn_paged_append(k.contiguous(), v.contiguous(), a[0], a[1], a[2], i32(cu),
+                                    i32(lens), max_n, q=q.contiguous(), inv_freq=f, **a[3])
+        got = ea.attn_paged_append(k, v, b[0], b[1], b[2], i32(cu), i32(lens), max_n, q=q, q_out=q,
+                                   inv_freq=f, **b[3])
+        assert torch.equal(got, want) and got.data_ptr() == dev.data_ptr()
+        assert torch.equal(dev[:, 4:].cpu(), qkv[:, 4:])
+        assert same_codes(a[0], b[0]) and same_codes(a[1], b[1])
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+def attend(c, q, n, *, hq, splits=0, max_k=None, **mask):
+    """Runs the kernel between guard bands and compares with the definition."""
+    cu = cu_of(n)
+    kc, vc, table, kw = c.to("cuda")
+    obuf, out, og = guarded_empty(q.shape, BF, kc.device)
+    lbuf, lse, lg = guarded_empty((hq, q.shape[0]), torch.float32, kc.device)
+    scale = q.shape[2] ** -0.5
+    ea.attn_paged_fwd(q.cuda(), kc, vc, table, i32(cu), i32(c.lens), max(n),
+                      max(c.lens) if max_k is None else max_k, num_splits=splits, out=out, lse=lse,
+                      scale=scale, **mask, **kw)
+    torch.cuda.synchronize()
+    assert guards_intact(obuf, og) and guards_intact(lbuf, lg)
+    ref, ref_lse, pabs = sr.attend(q, c.k, c.v, c.k_scale, c.v_scale, c.table, cu, c.lens, scale,
+                                   **mask)
+    compare(out[:cu[-1]], lse[:, :cu[-1]], ref[:cu[-1]], ref_lse[:, :cu[-1]], pabs[:cu[-1]], c.e4m3)
+    return out, lse
+
+
+def compare(out, lse, ref, ref_lse, pabs, e4m3):
+    out, lse = out.cpu().double(), lse.cpu().double()
+    assert torch.equal(out.isnan(), ref.isnan())
+    err = (out - ref).abs().nan_to_num(0.0)
+    bound = sr.o_bound(ref, pabs, e4m3).nan_to_num(1.0)
+    assert bool((err <= bound).all()), float((err / bound).max())
+    none = ref_lse == -math.inf
+    assert torch.equal(lse == -math.inf, none)
+    fine = torch.isfinite(ref_lse)
+    assert float((lse - ref_lse)[fine].abs().max() if fine.any() else 0.0) <= LSE_TOL
+
+
+GROUPS = [(4, 4), (8, 2), (8, 1), (5, 1), (6, 2)]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [16, 128])
+def test_single_tokens(d, e4m3, page):
+    lens = [1, 0, 2, 15, 16, 17, 63, 64, 65, 127, 128, 200, 600]
+    for i, (hq, hkv) in enumerate(GROUPS):
+        # NaN where no token is: it must not reach the result
+        c = Cache(lens, lens, hkv, d, page, e4m3, head_major=i % 2 == 0, seed=i, junk=math.nan)
+        q = rows(len(lens), hq, d, 10 + i, 0.2)
+        attend(c, q, [1] * len(lens), hq=hq, causal=i % 2 == 1)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("splits", [1, 2, 7, 128])
+def test_splits_give_the_same(d, e4m3, splits):
+    lens = [900, 3, 0, 257]
+    c = Cache(lens, lens, 2, d, 32, e4m3, seed=1, junk=math.nan)
+    q = rows(4, 8, d, 20, 0.2)
+    attend(c, q, [1] * 4, hq=8, splits=splits)
+    # a bound far above the lengths cuts them into empty parts
+    attend(c, q, [1] * 4, hq=8, splits=splits, max_k=50000)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("most", [2, 5, 13, 30])
+def test_several_rows(d, e4m3, most):
+    # rows of a group fill 8, 16, 32 and 64 columns, and more than one tile
+    n = [most, 0, 1, max(1, most - 1), 2]
+    lens = [300, 70, 0, most, 129]
+    for hq, hkv in ((4, 4), (8, 2), (5, 1)):
+        c = Cache(lens, lens, hkv, d, 64, e4m3, seed=most, junk=math.nan)
+        q = rows(sum(n) + 3, hq, d, 30 + most, 0.2)
+        attend(c, q, n, hq=hq, causal=True)
+        attend(c, q, n, hq=hq, causal=False, splits=3)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_rows_that_see_no_key(e4m3):
+    # more rows than keys: the first ones see none under a causal mask
+    n, lens = [6, 3, 1], [2, 0, 0]
+    c = Cache(lens, [16] * 3, 2, 64, 16, e4m3, seed=2, junk=math.nan)
+    q = rows(10, 4, 64, 40)
+    for splits in (0, 2):
+        out, lse = attend(c, q, n, hq=4, causal=True, splits=splits)
+        assert not out[:4].any() and bool((lse[:, :4] == -math.inf).all())
+        assert not out[6:].any() and bool((lse[:, 6:] == -math.inf).all())
+
+
+@pytest.mark.parametrize("d,e4m3", [(64, True), (128, False), (128, True), (256, True)])
+@pytest.mark.parametrize("window", [(0, 0), (1, -1), (15, 0), (64, 3), (100, -1), (-1, 2),
+                                    (500, 500)])
+def test_windows(d, e4m3, window):
+    n, lens = [1, 4, 12, 1], [333, 260, 12, 90]
+    c = Cache(lens, lens, 2, d, 32, e4m3, seed=4, junk=math.nan)
+    q = rows(sum(n), 6, d, 50, 0.2)
+    for causal in (False, True):
+        for splits in (0, 3):
+            attend(c, q, n, hq=6, causal=causal, window=window, splits=splits)
+
+
+@pytest.mark.parametrize("d,e4m3", [(64, False), (128, True), (256, True)])
+@pytest.mark.parametrize("cap", [1.5, 30.0])
+def test_softcap(d, e4m3, cap):
+    n, lens = [1, 5, 2], [200, 90, 2]
+    c = Cache(lens, lens, 1, d, 64, e4m3, seed=5)
+    q = rows(sum(n), 8, d, 60, 0.2)
+    attend(c, q, n, hq=8, causal=True, softcap=cap)
+    attend(c, q, n, hq=8, causal=True, softcap=cap, window=(50, -1), splits=2)
+
+
+def test_scales_far_apart():
+    # value scales 2^-40 .. 2^40 over the pages, and keys that favour any of them
+    d, page = 128, 16
+    lens = [400, 130]
+    c = Cache(lens, lens, 2, d, page, True, seed=6)
+    g = torch.Generator().manual_seed(6)
+    c.v_scale = 2.0 ** torch.randint(-40, 41, c.v_scale.shape, generator=g).float()
+    q = rows(2, 8, d, 70, 0.2)
+    attend(c, q, [1, 1], hq=8)
+    # queries of any size: the row is brought into f16's range by its own largest element
+    for f in (2.0 ** -60, 2.0 ** 12):
+        small = (rows(2, 8, d, 71, 0.2).double() * f).to(BF)
+        c2 = Cache(lens, lens, 2, d, page, True, seed=7)
+        c2.k_scale = c2.k_scale / f
+        attend(c2, small, [1, 1], hq=8)
+
+
+def test_one_heavy_key_among_many_light_ones():
+    # the light keys' weights are near 2^-20 of the heavy one's: together they count
+    d, n = 64, 20000
+    c = Cache([n], [n], 1, d, 128, True, seed=8, spread=0.0)
+    c.k[:] = 0.0
+    c.k[int(c.table[0, 5]), 17, 0] = torch.full((d,), 8.0).to(sr.E4M3)
+    c.k_scale[:] = 1.0
+    q = torch.full((1, 1, d), 13.9 / 64.0).to(BF)
+    attend(c, q, [1], hq=1)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_not_finite_keys_and_values(e4m3):
+    # NaN in a visible key or value reaches exactly the rows that see it
+    d, page = 64, 16
+    lens, n = [100, 50], [1, 1]
+    for where in ("k", "v"):
+        c = Cache(lens, lens, 2, d, page, e4m3, seed=9)
+        getattr(c, where)[int(c.table[1, 2]), 3, 1, 5] = math.nan
+        q = rows(2, 4, d, 80, 0.2)
+        kc, vc, table, kw = c.to("cuda")
+        out, lse = ea.attn_paged_fwd(q.cuda(), kc, vc, table, i32([0, 1, 2]), i32(lens), 1, 100,
+                                     **kw)
+        bad = out.isnan().cpu()
+        want = torch.zeros_like(bad)
+        if where == "k":
+            want[1, 2:] = True
+        else:
+            want[1, 2:, 5] = True
+        assert torch.equal(bad, want)
+
+
+def test_cut_off_lengths_and_bad_pages():
+    # lengths past the block table are cut there; pages outside the pool read as zeros
+    d, page = 128, 32
+    c = Cache([64, 50], [64, 64], 2, d, page, True, seed=10)
+    q = rows(2, 4, d, 90, 0.2)
+    kc, vc, table, kw = c.to("cuda")
+    args = (q.cuda(), kc, vc)
+    want = ea.attn_paged_fwd(*args, table, i32([0, 1, 2]), i32([64, 50]), 1, 64, **kw)
+    got = ea.attn_paged_fwd(*args, table, i32([0, 1, 2]), i32([1000, 50]), 1, 64, **kw)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    bad = table.clone()
+    bad[0, 1] = 10 ** 7
+    got = ea.attn_paged_fwd(*args, bad, i32([0, 1, 2]), i32([64, 50]), 1, 64, **kw)
+    assert torch.equal(want[0][1], got[0][1]) and bool(torch.isfinite(got[0]).all())
+
+
+def test_a_pool_past_32_bits():
+    # element offsets above 2^31 (a 2.4 GB pool), the last pages used
+    d, page, hkv = 128, 128, 8
+    pages = (1 << 31) // (page * hkv * d) + 2000
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("not enough memory")
+    dev = torch.device("cuda")
+    c = Cache([300], [300], hkv, d, page, True, seed=11, spare=0)
+    kc = torch.zeros(pages, hkv, page, d, dtype=sr.E4M3, device=dev).transpose(1, 2)
+    vc = torch.zeros_like(kc)
+    ks, vs = (torch.ones(pages, hkv, device=dev) for _ in range(2))
+    for i in range(c.pages):
+        at = pages - 1 - i
+        kc[at], vc[at], ks[at], vs[at] = (x[i].to(dev) for x in (c.k, c.v, c.k_scale, c.v_scale))
+    table = (pages - 1 - c.table).to(dev)
+    q = rows(1, 32, d, 100, 0.2)
+    k = rows(1, hkv, d, 101)
+    ea.attn_paged_append(k.cuda(), k.cuda(), kc, vc, table, i32([0, 1]), i32([300]), 1, k_scale=ks,
+                         v_scale=vs)
+    out, lse = ea.attn_paged_fwd(q.cuda(), kc, vc, table, i32([0, 1]), i32([300]), 1, 300,
+                                 k_scale=ks, v_scale=vs)
+    sr.append(k, c.k, c.k_scale, c.table, [0, 1], [300])
+    sr.append(k, c.v, c.v_scale, c.table, [0, 1], [300])
+    ref = sr.attend(q, c.k, c.v, c.k_scale, c.v_scale, c.table, [0, 1], [300], d ** -0.5)
+    compare(out, lse, *ref, True)
+
+
+def test_workspace_of_the_callers():
+    d, lens = 128, [700, 20]
+    c = Cache(lens, lens, 2, d, 64, True, seed=12)
+    q = rows(2, 8, d, 110, 0.2).cuda()
+    kc, vc, table, kw = c.to("cuda")
+    args = (q, kc, vc, table, i32([0, 1, 2]), i32(lens), 1, 700)
+    want = ea.attn_paged_fwd(*args, num_splits=5, **kw)
+    need = ea.paged_workspace_size(kc, vc, table, 2, 2, 1, 700, 8, num_splits=5, **kw)
+    assert need > 0
+    assert ea.paged_workspace_size(kc, vc, table, 2, 2, 1, 700, 8, num_splits=1, **kw) == 0
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # NaN wherever it is read
+    got = ea.attn_paged_fwd(*args, num_splits=5, workspace=ws, **kw)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    with pytest.raises(ea.AttnError):
+        ea.attn_paged_fwd(*args, num_splits=5, workspace=ws[:need - 256], **kw)
+
+
+def test_decoding_steps_equal_attention_over_the_whole():
+    """Prompts appended, then tokens one by one and a few at a time, in a captured
+    graph too: the attention over the bf16 cache equals attn_fwd on the rotated rows
+    within the rounding of P and O, and the e4m3 cache its own definition."""
+    hq, hkv, d, page = 8, 2, 128, 32
+    prompt, steps = [50, 7, 129], [1, 1, 3, 1]
+    total = [p + sum(steps) for p in prompt]
+    f = ea.rope_frequencies(d)[0].cuda()
+    q, k, v = (rows(sum(total), h, d, 200 + h, 0.2) for h in (hq, hkv, hkv + 1))
+    v = v[:, :hkv].contiguous()
+    cu_all = cu_of(total)
+    qr, kr = ea.attn_rotary(q.cuda(), k.cuda(), f, cu_seqlens=i32(cu_all))
+    full, full_lse = ea.attn_fwd(qr, kr, v.cuda(), i32(cu_all), i32(cu_all), max(total), max(total),
+                                 causal=True)
+    for e4m3 in (False, True):
+        c = Cache([0] * 3, total, hkv, d, page, e4m3, seed=13)
+        kc, vc, table, kw = c.to("cuda")
+        lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+        at = [0, 0, 0]
+        for step in [prompt] + [[s] * 3 for s in steps]:
+            cu = cu_of(step)
+            pick = torch.cat([torch.arange(cu_all[b] + at[b], cu_all[b] + at[b] + step[b])
+                              for b in range(3)])
+            at = [a + s for a, s in zip(at, step)]
+            lens += i32(step)
+            qo = ea.attn_paged_append(k[pick].cuda(), v[pick].cuda(), kc, vc, table, i32(cu), lens,
+                                      max(step), q=q[pick].cuda(), inv_freq=f, **kw)
+            assert torch.equal(qo, qr[pick.cuda()])
+            out, lse = ea.attn_paged_fwd(qo, kc, vc, table, i32(cu), lens, max(step), max(total),
+                                         causal=True, **kw)
+            scales = [x.cpu() for x in kw.values()] or [None, None]
+            ref = sr.attend(qo.cpu(), kc.cpu(), vc.cpu(), *scales, c.table, cu, at, d ** -0.5,
+                            causal=True)
+            compare(out, lse, *ref, e4m3)
+            if not e4m3:
+                # both are within the bound of the same reference
+                gap = (out - full[pick.cuda()]).abs().cpu().double()
+                assert bool((gap <= 2 * sr.o_bound(ref[0], ref[2], False)).all())
+                assert float((lse - full_lse[:, pick.cuda()]).abs().max()) <= 2 * LSE_TOL
+
+
+def test_a_captured_step_replays():
+    hq, hkv, d, page = 8, 2, 64, 16
+    lens0 = [30, 15, 200]
+    c = Cache(lens0, [x + 4 for x in lens0], hkv, d, page, True, seed=14)
+    f = ea.rope_frequencies(d)[0].cuda()
+    cu = i32([0, 1, 2, 3])
+    q, k, v = (rows(3, h, d, 300 + i).cuda() for i, h in enumerate((hq, hkv, hkv)))
+    a, b = c.to("cuda"), c.to("cuda")
+    lens_a, lens_b = i32(lens0), i32(lens0)
+
+    def step(pool, lens):
+        lens += 1
+        qo = ea.attn_paged_append(k, v, pool[0], pool[1], pool[2], cu, lens, 1, q=q, inv_freq=f,
+                                  **pool[3])
+        return ea.attn_paged_fwd(qo, pool[0], pool[1], pool[2], cu, lens, 1, 204, causal=True,
+                                 num_splits=2, **pool[3])
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(a, lens_a)
+    for i in range(4):
+        for x, h, s in ((q, hq, 0), (k, hkv, 1), (v, hkv, 2)):
+            x.copy_(rows(3, h, d, 400 + 10 * i + s))
+        graph.replay()
+        want = step(b, lens_b)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert same_codes(a[0], b[0]) and torch.equal(a[3]["v_scale"], b[3]["v_scale"])
