@@ -95,7 +95,18 @@ def library() -> ctypes.CDLL:
         lib.attn_bwd_static_scratch.restype = ctypes.c_int
         lib.attn_watchdog_selftest.argtypes = [i32, vp]
         lib.attn_watchdog_selftest.restype = ctypes.c_int
-        serving.declare(lib)
+        rows = [vp, ctypes.c_int64, ctypes.c_int64]  # pointer, token and head stride
+        lib.attn_rotary.argtypes = rows * 4 + [vp, i32, i32, f32, i32, vp, vp, vp, i32, i32, i32,
+                                               i32, i32, i32, vp]
+        lib.attn_rotary.restype = ctypes.c_int
+        lib.attn_paged_append.argtypes = [vp] + rows * 4 + [vp, vp, i32, i32, i32, i32, vp, i32,
+                                                            i32, f32, vp]
+        lib.attn_paged_append.restype = ctypes.c_int
+        lib.attn_paged_fwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32, i32,
+                                       f32, i32, i32, vp, vp, vp, ctypes.c_size_t, vp]
+        lib.attn_paged_fwd.restype = ctypes.c_int
+        lib.attn_paged_workspace_size.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, i32, i32]
+        lib.attn_paged_workspace_size.restype = ctypes.c_size_t
         _lib = lib
     return _lib
 
@@ -310,6 +321,6 @@ def attention(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, *
                             float(softcap or 0.0))
 
 
-from . import serving  # noqa: E402  (it uses the checks above)
+from . import serving  # noqa: E402, F401  (its binding is compiled: csrc/serving_binding.cpp)
 from .serving import (attn_paged_append, attn_paged_fwd, attn_rotary,  # noqa: E402
                       paged_workspace_size, rope_frequencies, rotary)

@@ -1,4 +1,5 @@
-"""Ahead-of-time build of libattn.so (sm_100a) with nvcc, in the source tree.
+"""Ahead-of-time build of libattn.so (sm_100a, nvcc) and of the compiled part of
+its Python binding, _serving.so (g++), in the source tree.
 
 Usage: python -m exact_attention_129_b200.build [--force] [--debug]
 """
@@ -17,6 +18,8 @@ LIB = os.path.join(HERE, "libattn.so")
 SOURCES = ["api.cu", "serve_api.cu"]
 HEADERS = ["ptx.cuh", "fwd_kernel.cuh", "fwd_pair_kernel.cuh", "bwd_kernels.cuh",
            "bwd_pair_kernel.cuh", "rotary.cuh", "paged_append.cuh", "paged_attn.cuh"]
+BINDING = os.path.join(HERE, "_serving.so")
+BINDING_SOURCE = os.path.join(CSRC, "serving_binding.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
@@ -38,8 +41,10 @@ def build(force: bool = False, verbose: bool = False, extra=(), out: str | None 
     """Compile libattn.so (or, with ``out``, a variant with the extra nvcc
     arguments ``extra``, e.g. ``-DATTN_FWD_POLY_PAIRS=2``, at that path)."""
     target = out or LIB
-    if out is None and not force and up_to_date():
-        return LIB
+    if out is None:
+        build_binding(force)
+        if not force and up_to_date():
+            return LIB
     tmp = target + f".tmp{os.getpid()}"
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
            "-std=c++17", "-t", "0", "-shared", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -53,6 +58,34 @@ def build(force: bool = False, verbose: bool = False, extra=(), out: str | None 
         sys.stderr.write(r.stdout + r.stderr)
     os.replace(tmp, target)
     return target
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile _serving.so against the installed torch; it calls libattn.so through
+    addresses it is given, so it does not link to it."""
+    inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "attn.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
+        return BINDING
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    includes = [INCLUDE, os.path.join(base, "include"),
+                os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{i}" for i in includes), BINDING_SOURCE, "-o", tmp,
+           f"-L{os.path.join(base, 'lib')}", "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed building _serving.so")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

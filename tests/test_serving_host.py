@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import exact_attention_129_b200 as ea
+from exact_attention_129_b200 import serving
 from exact_attention_129_b200 import build as eab
 from tests import serving_ref as sr
 
@@ -112,24 +113,48 @@ def test_paged_fwd_refuses(lib, bad):
 # ---------------------------------------------------------------------------
 # the binding
 # ---------------------------------------------------------------------------
-class Recorder:
-    def __init__(self):
-        self.calls = []
+class CacheStruct(ctypes.Structure):  # attn_paged_cache_t
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "block_table")] +
+                [(n, ctypes.c_int64) for n in ("k_s_page", "k_s_token", "k_s_head", "v_s_page",
+                                               "v_s_token", "v_s_head", "table_stride")] +
+                [(n, ctypes.c_int32) for n in ("type", "num_pages", "page_size", "pages_per_seq",
+                                               "nheads_kv", "head_dim")])
 
-    def __getattr__(self, name):
+
+class Recorder:
+    """Functions of the C ABI's types that write their arguments down, as callbacks."""
+
+    def __init__(self, lib):
+        vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+        cache, rows, size = ctypes.POINTER(CacheStruct), [vp, i64, i64], ctypes.c_size_t
+        types = {
+            "attn_rotary": [i32] + rows * 4 + [vp, i32, i32, f32, i32, vp, vp, vp] + [i32] * 6 + [vp],
+            "attn_paged_append": [i32, cache] + rows * 4 + [vp, vp, i32, i32, i32, i32, vp, i32, i32,
+                                                            f32, vp],
+            "attn_paged_fwd": [i32, cache, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32, i32,
+                               f32, i32, i32, vp, vp, vp, size, vp],
+            "attn_paged_workspace_size": [size, cache] + [i32] * 9,
+        }
+        self.calls, self.code = [], 0
+        self.functions = [ctypes.CFUNCTYPE(*types[n])(self._recorder(n)) for n in serving.ABI]
+        self.addresses = [ctypes.cast(f, ctypes.c_void_p).value for f in self.functions]
+
+    def _recorder(self, name):
         def f(*args):
+            args = tuple([getattr(a.contents, n) for n, _ in CacheStruct._fields_]
+                         if isinstance(a, ctypes.POINTER(CacheStruct)) else a for a in args)
             self.calls.append((name, args))
-            return 4096 if name.endswith("workspace_size") else 0
+            return 4096 if name.endswith("workspace_size") else self.code
         return f
 
 
 @pytest.fixture
-def rec(monkeypatch):
-    r = Recorder()
-    monkeypatch.setattr(ea, "library", lambda: r)
-    monkeypatch.setattr(ea, "_check_cuda", lambda *ts: None)
-    monkeypatch.setattr(ea, "_stream", lambda dev: None)
-    return r
+def rec(lib):
+    r = Recorder(lib)
+    binding = serving._binding or serving._load()
+    binding.init(ea.AttnError, *r.addresses, False)
+    yield r
+    serving._load()
 
 
 def _problem(t=5, hq=4, hkv=2, d=64, page=16, e4m3=True, lens=(9, 20)):
@@ -148,7 +173,7 @@ def test_binding_marshals_append_and_attention(rec):
                              q=p["q"], inv_freq=p["f"], mscale=1.5, interleaved=True, **p["kw"])
     name, a = rec.calls[-1]
     assert name == "attn_paged_append" and q.shape == p["q"].shape and q is not p["q"]
-    cache = struct.unpack("5P7q6i", a[0])
+    cache = tuple(a[0])
     assert cache[0] == p["kc"].data_ptr() and cache[2] == p["kw"]["k_scale"].data_ptr()
     assert cache[5:8] == (16 * 2 * 64, 64, 16 * 64)  # a head-major pool: page, token, head
     assert cache[11] == p["table"].shape[1]
