@@ -67,6 +67,7 @@ struct PagedParams {
   float cap_mul, cap_log2;  // softcap c: 2 / c, c log2(e); 0: none
   int hi_off, lo_off;      // as in FwdParams, kPagedNoBound: none
   int num_splits, chunk, row_tiles;
+  uint32_t k_page, k_token, v_page, v_token;  // strides in bytes
 };
 
 // keys of sequence b: what its row of the block table can hold, and under 2^29
@@ -83,11 +84,16 @@ struct PagedCfg {
   static constexpr int ROWB = D * ESZ;       // bytes of a cached row
   static constexpr int CPR = ROWB / 16;      // 16-byte pieces of it
   static constexpr int WK = 4 / WR;
-  static constexpr int BK = ROWB == 64 ? 128 : 64;  // keys per tile
+  // Tiles and stages measured on 16 sequences of 64K (e4m3, head_dim 128): 128
+  // keys x 2 stages 351 us, 128 x 3 382, 64 x 4 381: a third CTA on an SM (64 KB
+  // each) beats deeper stages.  Rows of 256 bytes: 64 x 2 334 us against 64 x 3
+  // 341 and 64 x 4 494 (128 ragged sequences in bf16).  Rows of 64 bytes: 3
+  // stages 91 us, 2 stages 93.
+  static constexpr int BK = ROWB <= 128 ? 128 : 64;  // keys per tile
   static constexpr int KT = BK / WK / 16;    // 16-key blocks per warp and tile
   static constexpr int RT = 8 * NT * WR;     // query rows per CTA
   static constexpr int TILE = BK * ROWB;
-  static constexpr int STAGES = ROWB >= 256 ? 3 : 4;
+  static constexpr int STAGES = ROWB == 64 ? 3 : 2;
   static constexpr int STAGE = 2 * TILE + 2 * (BK / 16) * 4;  // K, V, their scales
   static constexpr int QROW = D + 8;         // padded, in elements
   static constexpr int OROW = D + 4;
@@ -231,6 +237,8 @@ __global__ void __launch_bounds__(128) attn_paged_kernel(const PagedParams p) {
     const int64_t t = g / p.hq;
     p.lse[(g - t * p.hq) * static_cast<int64_t>(p.total_q) + t] = l2 * 0.6931471805599453f;
   };
+  // the merge may be put on the SMs as they empty; it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (kb64 >= ke) {  // no key of this part is seen
     if (p.num_splits > 1) {
       if (tid < rows)
@@ -246,50 +254,59 @@ __global__ void __launch_bounds__(128) attn_paged_kernel(const PagedParams p) {
   const int kb = static_cast<int>(kb64);
   const int tiles = (ke - kb + BK - 1) / BK;
 
-  // ---- loads
-  const uint8_t* kbase = p.kc.p + p.kc.s_head * C::ESZ * h;
-  const uint8_t* vbase = p.vc.p + p.vc.s_head * C::ESZ * h;
+  // ---- loads: 32-bit products of a page or slot with a stride, added to 64-bit bases
+  const uint8_t* kbase = p.kc.p + p.kc.s_head * C::ESZ * h + (tid % CPR) * 16;
+  const uint8_t* vbase = p.vc.p + p.vc.s_head * C::ESZ * h + (tid % CPR) * 16;
   const int32_t* table = p.table + b * p.table_stride;
   const int slot_mask = (1 << p.page_shift) - 1;
+  const int row_in_tile = tid / CPR;
+  auto swizzle = [](int row, int c) -> uint32_t {
+    if constexpr (C::ROWB >= 128) {
+      return row * C::ROWB + ((c ^ (row & 7)) << 4);
+    } else {
+      const uint32_t o = row * C::ROWB + (c << 4);
+      return o ^ (((o >> 7) & 7) << 4);
+    }
+  };
+  uint32_t dst[BK * CPR / 128];
+#pragma unroll
+  for (int i = 0; i < BK * CPR / 128; ++i)
+    dst[i] = sbase + swizzle(row_in_tile + i * (128 / CPR), tid % CPR);
+  const uint32_t spread = ke - klo;
   auto issue = [&](int t) {
-    const uint32_t st = sbase + (t % C::STAGES) * C::STAGE;
-    const int c = tid % CPR;
+    const uint32_t st = (t % C::STAGES) * C::STAGE;
+    const int key0 = kb + t * BK;
 #pragma unroll
     for (int i = 0; i < BK * CPR / 128; ++i) {
-      const int row = tid / CPR + i * (128 / CPR);
-      const int key = kb + t * BK + row;
-      bool live = key >= klo && key < ke;
-      int page = 0;
+      const int key = key0 + row_in_tile + i * (128 / CPR);
+      uint32_t page = 0;
+      bool live = static_cast<uint32_t>(key - klo) < spread;
       if (live) {
         page = __ldg(table + (key >> p.page_shift));
-        live = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
-        if (!live) page = 0;
+        live = page < static_cast<uint32_t>(p.num_pages);
       }
-      const int slot = key & slot_mask;
-      uint32_t o;
-      if constexpr (C::ROWB >= 128) {
-        o = row * C::ROWB + ((c ^ (row & 7)) << 4);
-      } else {
-        o = row * C::ROWB + (c << 4);
-        o ^= ((o >> 7) & 7) << 4;
-      }
-      pg_cp16(st + o, kbase + (page * p.kc.s_page + slot * p.kc.s_token) * C::ESZ + c * 16, live);
-      pg_cp16(st + C::TILE + o, vbase + (page * p.vc.s_page + slot * p.vc.s_token) * C::ESZ + c * 16,
+      if (!live) page = 0;
+      const uint32_t slot = key & slot_mask;
+      pg_cp16(st + dst[i],
+              kbase + static_cast<uint64_t>(page) * p.k_page + static_cast<uint64_t>(slot) * p.k_token,
+              live);
+      pg_cp16(st + C::TILE + dst[i],
+              vbase + static_cast<uint64_t>(page) * p.v_page + static_cast<uint64_t>(slot) * p.v_token,
               live);
     }
     if constexpr (FP8) {
       if (tid < 2 * (BK / 16)) {
-        const int blk = tid >> 1, key = kb + t * BK + blk * 16;
-        bool live = key < ke;  // a block of 16 keys lies in one page
-        int page = 0;
+        const int key = key0 + (tid >> 1) * 16;  // a block of 16 keys lies in one page
+        uint32_t page = 0;
+        bool live = key < ke;
         if (live) {
           page = __ldg(table + (key >> p.page_shift));
-          live = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
-          if (!live) page = 0;
+          live = page < static_cast<uint32_t>(p.num_pages);
         }
+        if (!live) page = 0;
         const float* src = ((tid & 1) ? p.vc.scale : p.kc.scale) +
                            static_cast<int64_t>(page) * p.hkv + h;
-        pg_cp4(st + 2 * C::TILE + tid * 4, src, live);
+        pg_cp4(sbase + st + 2 * C::TILE + tid * 4, src, live);
       }
     }
   };
@@ -379,14 +396,7 @@ __global__ void __launch_bounds__(128) attn_paged_kernel(const PagedParams p) {
   // the lane's row and piece of the 8x8 matrices: K: keys, then pieces; V (bf16):
   // pieces, then keys; V (e4m3) as K
   const int mat = lane >> 3, in8 = lane & 7;
-  auto piece = [&](uint32_t base, int row, int c) {
-    if constexpr (C::ROWB >= 128) {
-      return base + row * C::ROWB + ((c ^ (row & 7)) << 4);
-    } else {
-      const uint32_t off = row * C::ROWB + (c << 4);
-      return base + (off ^ (((off >> 7) & 7) << 4));
-    }
-  };
+  auto piece = [&](uint32_t base, int row, int c) { return base + swizzle(row, c); };
 
   for (int t = 0; t < tiles; ++t) {
     pg_wait<C::STAGES - 2>();
@@ -401,12 +411,17 @@ __global__ void __launch_bounds__(128) attn_paged_kernel(const PagedParams p) {
 
     float s[KT][NT][4];
     float vs[KT];
+    // two chains of MMAs per score where there are few: half the latency
+    constexpr int CH = KT * NT <= 2 ? 2 : 1;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
+      float acc[CH][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[kt][nt][x] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[ch][nt][x] = 0.f;
       const int row = wk * KT * 16 + kt * 16 + (mat & 1) * 8 + in8;
 #pragma unroll
       for (int pr = 0; pr < CPR / 2; ++pr) {
@@ -424,7 +439,7 @@ __global__ void __launch_bounds__(128) attn_paged_kernel(const PagedParams p) {
                 b0 = qf[nt][2 * pr + u][0], b1 = qf[nt][2 * pr + u][1];
               else
                 q_frag(nt, 2 * pr + u, b0, b1);
-              pg_mma<true>(s[kt][nt], a0, a1, a2, a3, b0, b1);
+              pg_mma<true>(acc[u % CH][nt], a0, a1, a2, a3, b0, b1);
             }
           }
         } else {
@@ -435,10 +450,15 @@ __global__ void __launch_bounds__(128) attn_paged_kernel(const PagedParams p) {
               b0 = qf[nt][pr][0], b1 = qf[nt][pr][1];
             else
               q_frag(nt, pr, b0, b1);
-            pg_mma<false>(s[kt][nt], a[0], a[1], a[2], a[3], b0, b1);
+            pg_mma<false>(acc[pr % CH][nt], a[0], a[1], a[2], a[3], b0, b1);
           }
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[kt][nt][x] = CH == 2 ? acc[0][nt][x] + acc[CH - 1][nt][x]
+                                                          : acc[0][nt][x];
     }
     // scores in log2 units; the maximum of score + exponent of the V scale
     float mx[NT][2];
@@ -450,27 +470,38 @@ __global__ void __launch_bounds__(128) attn_paged_kernel(const PagedParams p) {
       float ks = 1.f, lv = 0.f;
       vs[kt] = 1.f;
       if constexpr (FP8) {
-        ks = scales[2 * (wk * KT + kt)];
-        vs[kt] = scales[2 * (wk * KT + kt) + 1];
+        const float2 sc = *reinterpret_cast<const float2*>(scales + 2 * (wk * KT + kt));
+        ks = sc.x;
+        vs[kt] = sc.y;
         // (a page outside the pool has scales of 0: its keys count as x = 0)
         if (vs[kt] != 0.f)
           lv = static_cast<float>(static_cast<int>(__float_as_uint(vs[kt]) >> 23) - 127);
       }
-      const bool edge = k0 < in_lo || k0 + 16 > in_hi || k0 + 16 > ke;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int j = x & 1;
-          float v = s[kt][nt][x] * (rf[nt][j] * ks);
-          if (capped) v = pg_cap(v * p.cap_mul, p.cap_log2);
-          if (edge) {
+        for (int x = 0; x < 4; ++x) s[kt][nt][x] *= rf[nt][x & 1] * ks;
+      if (capped) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[kt][nt][x] = pg_cap(s[kt][nt][x] * p.cap_mul, p.cap_log2);
+      }
+      if (k0 < in_lo || k0 + 16 > in_hi || k0 + 16 > ke) {  // some row does not see some key
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
             const int key = k0 + oct + (x >> 1) * 8;
-            if (key < lo[nt][j] || key > hi[nt][j] || key >= ke) v = -INFINITY;
+            if (key < lo[nt][x & 1] || key > hi[nt][x & 1] || key >= ke)
+              s[kt][nt][x] = -INFINITY;
           }
-          s[kt][nt][x] = v;
-          mx[nt][j] = fmaxf(mx[nt][j], v + lv);
-        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          mx[nt][j] = fmaxf(mx[nt][j], fmaxf(s[kt][nt][j], s[kt][nt][j + 2]) + lv);
     }
     bool raise = false;
 #pragma unroll
@@ -614,63 +645,72 @@ __global__ void __launch_bounds__(128) attn_paged_kernel(const PagedParams p) {
   }
 }
 
-// O = sum_s 2^(lse_s - lse) O_s, lse = log2 sum_s 2^lse_s; one warp per packed
-// (row, head) of the rows that belong to a sequence.  A part without a key has
-// lse = -inf and its O is not read.
+// O = sum_s 2^(lse_s - lse) O_s, lse = log2 sum_s 2^lse_s for one packed (row,
+// head) per CTA: D / 4 threads cover the head and the CTA's groups of them take
+// every GROUPS-th part, so that a row of many parts is read in a few rounds.
+// A part without a key has lse = -inf and its O is not read.  Launched so that
+// its start overlaps the end of the attention kernel, whose results it waits for.
 template <int D>
-__global__ void __launch_bounds__(128) attn_paged_merge_kernel(const PagedParams p, int batch) {
-  const int lane = threadIdx.x & 31;
-  const int64_t g = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(256) attn_paged_merge_kernel(const PagedParams p, int batch) {
+  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+  __shared__ float w[128];
+  __shared__ float sums[2];
+  __shared__ float4 part[GROUPS][LANES];
+  const int64_t g = blockIdx.x;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.hq;
   const int64_t t = g / p.hq;
-  if (g >= rows || t < p.cu[0] || t >= p.cu[batch]) return;
-  float ls[4], top = -INFINITY;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (t < p.cu[0] || t >= p.cu[batch]) return;
+  const int tid = threadIdx.x, n = p.num_splits;
+  if (tid < 32) {
+    float ls[4], top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int s = i * 32 + lane;
-    ls[i] = s < p.num_splits ? p.part_lse[s * rows + g] : -INFINITY;
-    // a NaN part has to win: its row is NaN
-    top = fmaxf(top, ls[i]);
-  }
+    for (int i = 0; i < 4; ++i) {
+      const int s = i * 32 + tid;
+      ls[i] = s < n ? p.part_lse[s * rows + g] : -INFINITY;
+      top = fmaxf(top, ls[i]);
+    }
 #pragma unroll
-  for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    ls[i] = pg_ex2(ls[i] - base);
-    sum += ls[i];
-  }
+    for (int i = 0; i < 4; ++i) {
+      ls[i] = pg_ex2(ls[i] - base);  // NaN where a part is NaN: its row is NaN
+      sum += ls[i];
+      w[i * 32 + tid] = ls[i];
+    }
 #pragma unroll
-  for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-  constexpr int E = D / 32;
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = min(32, p.num_splits - i * 32);
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float w = __shfl_sync(0xffffffffu, ls[i], s);
-      if (w == 0.f) continue;  // NaN is not 0
-      const float* src = p.part_o + ((i * 32 + s) * rows + g) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + e);
-        acc[e] += w * v.x;
-        acc[e + 1] += w * v.y;
-      }
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    if (tid == 0) {
+      sums[0] = sum == 0.f ? 0.f : 1.f / sum;
+      if (p.lse)
+        p.lse[(g - t * p.hq) * static_cast<int64_t>(p.total_q) + t] =
+            sum == 0.f ? -INFINITY : (base + pg_lg2(sum)) * 0.6931471805599453f;
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t* dst = p.out + g * D + lane * E;
+  __syncthreads();
+  const int c = tid % LANES, grp = tid / LANES;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = grp; s < n; s += GROUPS) {
+    const float f = w[s];
+    if (f == 0.f) continue;
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (s * rows + g) * D + c * 4);
+    a.x += f * v.x, a.y += f * v.y, a.z += f * v.z, a.w += f * v.w;
+  }
+  part[grp][c] = a;
+  __syncthreads();
+  if (grp == 0) {
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = bf16_pair(acc[e] * inv, acc[e + 1] * inv);
-  if (p.lse && lane == 0)
-    p.lse[(g - t * p.hq) * static_cast<int64_t>(p.total_q) + t] =
-        sum == 0.f ? -INFINITY : (base + pg_lg2(sum)) * 0.6931471805599453f;
+    for (int i = 1; i < GROUPS; ++i) {
+      const float4 v = part[i][c];
+      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+    }
+    const float inv = sums[0];
+    *reinterpret_cast<uint2*>(p.out + g * D + c * 4) =
+        make_uint2(bf16_pair(a.x * inv, a.y * inv), bf16_pair(a.z * inv, a.w * inv));
+  }
 }
 
 }  // namespace attn

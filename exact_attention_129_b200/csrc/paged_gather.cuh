@@ -1,0 +1,121 @@
+// paged_gather.cuh -- a paged cache's keys and values as packed bf16 rows, for
+// calls with many query rows per sequence: those are bound by the tensor cores,
+// so the keys are brought once into the layout of attn_fwd, whose tcgen05
+// kernels run several times the rate of the mma.sync kernel in paged_attn.cuh.
+// The pass reads a code (1 or 2 bytes) and writes 2 bytes per element: HBM-bound.
+//
+// e4m3: code * scale rounded to bf16, exact for a power-of-two scale (a code has
+// 4 significant bits).
+//
+// Sequence b becomes segment 2b of the packed problem, followed by segment
+// 2b + 1 of no queries and kGatherPad zero rows.  attn_fwd reads whole blocks of
+// up to 128 keys, multiplying those behind a segment's end by zero weights: they
+// are these zeros and never another sequence's rows, whose NaN would survive
+// the product.  Under a window the rows more than 128 below the first visible
+// key are not needed and not copied.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "paged_attn.cuh"
+
+namespace attn {
+
+constexpr int kGatherPad = 128;
+constexpr int kGatherThreads = 256;
+
+struct GatherParams {
+  PagedParams a;       // cache, table, lengths, lo_off
+  int batch, max_k;
+  uint16_t* k;         // [rows][hkv][D]
+  uint16_t* v;
+  int32_t* cu_q;       // [2 batch + 1]
+  int32_t* cu_k;
+};
+
+__device__ __forceinline__ int gather_length(const GatherParams& p, int b) {
+  return min(paged_length(p.a, b), p.max_k);
+}
+
+// grid: (pages and pad of the longest sequence, sequences, K and V)
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kGatherThreads) attn_paged_gather_kernel(const GatherParams p) {
+  const int b = blockIdx.y, tid = threadIdx.x;
+  const int n = gather_length(p, b);
+  const int page_size = 1 << p.a.page_shift;
+  const int first = blockIdx.x * page_size;
+  const bool header = blockIdx.x == 0 && blockIdx.z == 0;
+  if (first >= n + kGatherPad && !header) return;
+  // packed row of the sequence's first key
+  __shared__ int64_t part[kGatherThreads / 32];
+  int64_t sum = 0;
+  for (int i = tid; i < b; i += kGatherThreads) sum += gather_length(p, i) + kGatherPad;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((tid & 31) == 0) part[tid >> 5] = sum;
+  __syncthreads();
+  int64_t row0 = 0;
+#pragma unroll
+  for (int i = 0; i < kGatherThreads / 32; ++i) row0 += part[i];
+  if (header && tid == 0) {
+    p.cu_q[2 * b] = p.a.cu[b];
+    p.cu_q[2 * b + 1] = p.a.cu[b + 1];
+    p.cu_k[2 * b] = static_cast<int32_t>(row0);
+    p.cu_k[2 * b + 1] = static_cast<int32_t>(row0 + n);
+    if (b == p.batch - 1) {
+      p.cu_q[2 * b + 2] = p.a.cu[b + 1];
+      p.cu_k[2 * b + 2] = static_cast<int32_t>(row0 + n + kGatherPad);
+    }
+  }
+  const int nq = p.a.cu[b + 1] - p.a.cu[b];
+  if (nq <= 0) return;  // no row reads these keys
+  int low = 0;
+  if (p.a.lo_off < kPagedNoBound) low = max(0, n - nq - p.a.lo_off - 128);
+  const int last = min(first + page_size, n + kGatherPad);
+  if (last <= low) return;
+  const bool is_v = blockIdx.z != 0;
+  const CacheView& c = is_v ? p.a.vc : p.a.kc;
+  int page = -1;
+  if (first < n) page = p.a.table[b * p.a.table_stride + blockIdx.x];
+  const bool known = static_cast<unsigned>(page) < static_cast<unsigned>(p.a.num_pages);
+  constexpr int PIECES = D / 16;  // 16 elements each
+  const int items = (last - first) * p.a.hkv * PIECES;
+  uint16_t* out = (is_v ? p.v : p.k) + (row0 + first) * p.a.hkv * D;
+  for (int x = tid; x < items; x += kGatherThreads) {
+    const int piece = x % PIECES, rh = x / PIECES;
+    const int h = rh % p.a.hkv, slot = rh / p.a.hkv;
+    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+    if (first + slot < n && known) {
+      const int64_t at = page * c.s_page + slot * c.s_token + h * c.s_head + piece * 16;
+      if constexpr (FP8) {
+        const uint4 w = *reinterpret_cast<const uint4*>(c.p + at);
+        const float s = c.scale[static_cast<int64_t>(page) * p.a.hkv + h];
+        auto four = [&](uint32_t codes, uint32_t& a, uint32_t& b2) {
+          const uint32_t h0 = pg_f16_lo(codes), h1 = pg_f16_hi(codes);
+          float f0, f1, f2, f3;
+          asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}"
+              : "=f"(f0), "=f"(f1) : "r"(h0));
+          asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}"
+              : "=f"(f2), "=f"(f3) : "r"(h1));
+          a = bf16_pair(f0 * s, f1 * s);
+          b2 = bf16_pair(f2 * s, f3 * s);
+        };
+        four(w.x, lo.x, lo.y);
+        four(w.y, lo.z, lo.w);
+        four(w.z, hi.x, hi.y);
+        four(w.w, hi.z, hi.w);
+      } else {
+        const uint4* src = reinterpret_cast<const uint4*>(c.p + at * 2);
+        lo = src[0];
+        hi = src[1];
+      }
+    }
+    uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(x) * 16);
+    dst[0] = lo;
+    dst[1] = hi;
+  }
+}
+
+}  // namespace attn

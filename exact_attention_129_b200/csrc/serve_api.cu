@@ -9,6 +9,7 @@
 #include "attn.h"
 #include "paged_append.cuh"
 #include "paged_attn.cuh"
+#include "paged_gather.cuh"
 #include "rotary.cuh"
 
 namespace attn {
@@ -16,6 +17,7 @@ namespace {
 
 constexpr int kServeDevices = 64;
 constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int64_t kMaxStride = int64_t(1) << 31;  // elements: the kernels' bytes fit 32 bits
 
 struct ServeDevice {
   int major = 0, sms = 0;
@@ -92,7 +94,7 @@ attn_status_t check_cache(const attn_paged_cache_t* c) {
   const int64_t step = e4m3 ? 16 : 8;  // 16-byte accesses everywhere
   for (int64_t s : {c->k_s_page, c->k_s_token, c->k_s_head, c->v_s_page, c->v_s_token,
                     c->v_s_head})
-    if (s % step != 0) return ATTN_ERR_INVALID_ARG;
+    if (s % step != 0 || s < 0 || s >= kMaxStride) return ATTN_ERR_INVALID_ARG;
   if (c->num_pages < 0 || c->pages_per_seq < 0 || c->nheads_kv < 1 || c->nheads_kv > 65535)
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
@@ -176,8 +178,19 @@ attn_status_t launch_append(const AppendParams& p, bool e4m3, int max_seqlen, in
 // ---------------------------------------------------------------------------
 constexpr int kPagedMaxSplits = 128;
 
+// Many query rows per sequence go through packed bf16 keys (paged_gather.cuh)
+// and attn_fwd: from kDenseRows rows of a group on, unless the packed copies
+// would take more than kDenseBytes.
+constexpr int64_t kDenseRows = 128;
+constexpr int64_t kDenseBytes = int64_t(4) << 30;
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
 // how a call is cut into CTAs; a pure function of the arguments and the device
 struct PagedPlan {
+  bool dense;          // gather, then attn_fwd
+  int64_t key_rows;    // of the packed copies
+  size_t v_off, cu_q_off, cu_k_off;
   int nt, wr;          // query rows per CTA: 8 nt wr
   int row_tiles;
   int splits, chunk;   // parts of the keys, and their length
@@ -187,9 +200,20 @@ struct PagedPlan {
 // requested splits 0: enough parts for about two rounds of CTAs, of at least 256 keys
 PagedPlan paged_plan(const attn_paged_cache_t* c, int batch, int total_q, int max_q, int max_k,
                      int hq, int hi_off, int lo_off, int want, int sms) {
-  PagedPlan pl;
+  PagedPlan pl{};
   const int64_t group = hq / c->nheads_kv;
   const int64_t rows = group * max_q;
+  pl.key_rows = static_cast<int64_t>(batch) * (static_cast<int64_t>(max_k) + kGatherPad);
+  const int64_t copy = pl.key_rows * c->nheads_kv * c->head_dim * 2;
+  pl.dense = want == 0 && rows >= kDenseRows && batch <= 32767 && 2 * copy <= kDenseBytes &&
+             pl.key_rows < (int64_t(1) << 30);
+  if (pl.dense) {
+    pl.v_off = align256(copy);
+    pl.cu_q_off = pl.v_off + align256(copy);
+    pl.cu_k_off = pl.cu_q_off + align256((2 * static_cast<size_t>(batch) + 1) * 4);
+    pl.bytes = pl.cu_k_off + align256((2 * static_cast<size_t>(batch) + 1) * 4);
+    return pl;
+  }
   pl.nt = rows <= 8 ? 1 : 2;
   pl.wr = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   const int rt = 8 * pl.nt * pl.wr;
@@ -201,7 +225,7 @@ PagedPlan paged_plan(const attn_paged_cache_t* c, int batch, int total_q, int ma
                                        (rt + group - 1) / group + 1);
   if (lo_off < kPagedNoBound) span += 15;  // parts begin at a multiple of 16
   span = std::max<int64_t>(span, 1);
-  const int bk = (c->type == ATTN_CACHE_E4M3 && c->head_dim == 64) ? 128 : 64;
+  constexpr int bk = 128;  // parts end at a whole number of tiles of every kernel
   const int64_t ctas = static_cast<int64_t>(batch) * c->nheads_kv * pl.row_tiles;
   int64_t splits = want;
   if (want == 0) {
@@ -217,6 +241,15 @@ PagedPlan paged_plan(const attn_paged_cache_t* c, int batch, int total_q, int ma
   pl.lse_off = (rows_all * c->head_dim * 4 + 255) / 256 * 256;
   pl.bytes = pl.splits > 1 ? pl.lse_off + rows_all * 4 : 0;
   return pl;
+}
+
+template <int D, bool FP8>
+attn_status_t launch_gather(const GatherParams& p, cudaStream_t s) {
+  const int page = 1 << p.a.page_shift;
+  const int64_t pages = (static_cast<int64_t>(p.max_k) + kGatherPad + page - 1) / page;
+  attn_paged_gather_kernel<D, FP8>
+      <<<dim3(static_cast<unsigned>(pages), p.batch, 2), kGatherThreads, 0, s>>>(p);
+  return launched();
 }
 
 struct PagedMask {
@@ -258,9 +291,20 @@ attn_status_t launch_paged(const PagedParams& p, int batch, cudaStream_t s) {
   attn_paged_kernel<D, FP8, NT, WR><<<static_cast<unsigned>(ctas), 128, C::SMEM, s>>>(p);
   attn_status_t st = launched();
   if (st != ATTN_OK || p.num_splits == 1) return st;
-  const int64_t warps = static_cast<int64_t>(p.total_q) * p.hq;
-  attn_paged_merge_kernel<D><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, s>>>(p, batch);
-  return launched();
+  const int64_t rows = static_cast<int64_t>(p.total_q) * p.hq;
+  if (rows > kMaxGrid) return ATTN_ERR_INVALID_ARG;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_paged_merge_kernel<D>, p, batch) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
 }
 
 template <int D, bool FP8>
@@ -453,8 +497,34 @@ extern "C" attn_status_t attn_paged_fwd(
   p.num_splits = pl.splits;
   p.chunk = pl.chunk;
   p.row_tiles = pl.row_tiles;
+  const uint32_t esz = cache->type == ATTN_CACHE_E4M3 ? 1 : 2;
+  p.k_page = static_cast<uint32_t>(cache->k_s_page) * esz;
+  p.k_token = static_cast<uint32_t>(cache->k_s_token) * esz;
+  p.v_page = static_cast<uint32_t>(cache->v_s_page) * esz;
+  p.v_token = static_cast<uint32_t>(cache->v_s_token) * esz;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->type == ATTN_CACHE_E4M3;
+  if (pl.dense) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    GatherParams g;
+    g.a = p;
+    g.batch = batch;
+    g.max_k = max_seqlen_k;
+    g.k = reinterpret_cast<uint16_t*>(ws);
+    g.v = reinterpret_cast<uint16_t*>(ws + pl.v_off);
+    g.cu_q = reinterpret_cast<int32_t*>(ws + pl.cu_q_off);
+    g.cu_k = reinterpret_cast<int32_t*>(ws + pl.cu_k_off);
+    switch (cache->head_dim) {
+      case 64: st = e4m3 ? launch_gather<64, true>(g, s) : launch_gather<64, false>(g, s); break;
+      case 128: st = e4m3 ? launch_gather<128, true>(g, s) : launch_gather<128, false>(g, s); break;
+      default: st = e4m3 ? launch_gather<256, true>(g, s) : launch_gather<256, false>(g, s);
+    }
+    if (st != ATTN_OK) return st;
+    return attn_fwd_ex(q, g.k, g.v, g.cu_q, g.cu_k, 2 * batch, total_q,
+                       static_cast<int32_t>(pl.key_rows), max_seqlen_q, max_seqlen_k, nheads_q,
+                       cache->nheads_kv, cache->head_dim, scale, causal, window_left, window_right,
+                       softcap, return_lse, out, lse, stream);
+  }
   switch (cache->head_dim) {
     case 64:
       return e4m3 ? launch_paged_rows<64, true>(p, pl, batch, s)

@@ -312,8 +312,8 @@ attn_status_t attn_rotary(const void* q, int64_t q_st, int64_t q_sh, const void*
  *
  *   k, v         element (page, token of the page, head, d) is at
  *                page * s_page + token * s_token + head * s_head + d; the
- *                strides are in elements, their bytes multiples of 16, the
- *                pointers 16-byte aligned.  Any order of the three outer
+ *                strides are in elements, 0 to 2^31 - 1, their bytes multiples of
+ *                16, the pointers 16-byte aligned.  Any order of the three outer
  *                dimensions serves; heads before tokens keeps a page's rows of
  *                one head together, which the attention reads a little faster.
  *   type         ATTN_CACHE_BF16, or ATTN_CACHE_E4M3: 8-bit floats whose value
