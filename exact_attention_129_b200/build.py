@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libattn.so")
 SOURCES = ["api.cu", "serve_api.cu"]
 HEADERS = ["ptx.cuh", "fwd_kernel.cuh", "fwd_pair_kernel.cuh", "bwd_kernels.cuh",
-           "bwd_pair_kernel.cuh", "rotary.cuh", "paged_append.cuh", "paged_attn.cuh",
+           "bwd_pair_kernel.cuh", "rotary.cuh", "paged_append.cuh", "paged_common.cuh",
+           "paged_attn.cuh",
            "paged_gather.cuh"]
 BINDING = os.path.join(HERE, "_serving.so")
 BINDING_SOURCE = os.path.join(CSRC, "serving_binding.cpp")

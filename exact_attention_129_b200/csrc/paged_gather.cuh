@@ -19,7 +19,7 @@
 
 #include <cstdint>
 
-#include "paged_attn.cuh"
+#include "paged_common.cuh"
 
 namespace attn {
 

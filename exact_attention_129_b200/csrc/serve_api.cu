@@ -178,68 +178,153 @@ attn_status_t launch_append(const AppendParams& p, bool e4m3, int max_seqlen, in
 // ---------------------------------------------------------------------------
 constexpr int kPagedMaxSplits = 128;
 
-// Many query rows per sequence go through packed bf16 keys (paged_gather.cuh)
-// and attn_fwd: from kDenseRows rows of a group on, unless the packed copies
-// would take more than kDenseBytes.
-constexpr int64_t kDenseRows = 128;
-constexpr int64_t kDenseBytes = int64_t(4) << 30;
+// How a call is cut into CTAs, a pure function of the arguments and the device.
+// Two ways are open: the paged kernel over parts of the keys (with a merge), and
+// packed bf16 copies (paged_gather.cuh) with attn_fwd.  Both are estimated from
+// rates measured on a B200 and the quicker one is taken.
+struct PagedPlan {
+  bool dense;
+  int splits;          // parts of the keys (dense: of attn_fwd_split)
+  // paged kernel
+  int rt;              // query rows per CTA
+  int row_tiles;
+  int chunk;           // keys of a part
+  size_t lse_off;      // workspace: partial O, then partial LSE
+  // dense
+  int64_t key_rows;    // of the packed copies
+  size_t v_off, cu_q_off, cu_k_off, split_off, split_bytes;
+  size_t bytes;        // of the workspace
+};
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// how a call is cut into CTAs; a pure function of the arguments and the device
-struct PagedPlan {
-  bool dense;          // gather, then attn_fwd
-  int64_t key_rows;    // of the packed copies
-  size_t v_off, cu_q_off, cu_k_off;
-  int nt, wr;          // query rows per CTA: 8 nt wr
-  int row_tiles;
-  int splits, chunk;   // parts of the keys, and their length
-  size_t lse_off, bytes;  // workspace: partial O, then partial LSE
+constexpr double kHbmBytesPerNs = 6500.0;   // measured copy rate
+constexpr int64_t kDenseBytes = int64_t(4) << 30;  // the packed copies may take so much
+
+// ns per key of one CTA of the paged kernel, by head_dim 64, 128, 256 and 8, 16,
+// 32, 64 rows: the same, up to a tenth, with one or two CTAs on an SM
+constexpr double kPagedNsPerKey[3][4] = {{8.4, 9.6, 15., 26.}, {12., 15., 22., 37.},
+                                         {21., 27., 36., 63.}};
+// ns per key of one CTA of attn_fwd (its query tile against one key)
+constexpr double kDenseNsPerKey[3] = {15., 17.7, 21.};
+
+struct PagedShape {
+  int64_t batch, units, group, rows, max_k, span, total_q, hq;
+  int d, d_index, key_bytes;  // key_bytes: of K and V of one key and head
 };
 
-// requested splits 0: enough parts for about two rounds of CTAs, of at least 256 keys
+constexpr double kRoundNs = 3000.0;  // a CTA's set-up and drain
+constexpr double kMergeCopies = 3.0;  // the parts of O cross HBM or L2 about so often
+
+// one round of k CTAs of chunk keys side by side
+double round_ns(int64_t k, double chunk, double ns_per_key, double key_bytes) {
+  return kRoundNs + std::max(chunk * ns_per_key, k * chunk * key_bytes / kHbmBytesPerNs);
+}
+// n CTAs of equal length: whole rounds of `slots`, then the rest
+double rounds_ns(int64_t n, int64_t slots, double chunk, double ns_per_key, double key_bytes) {
+  const int64_t full = n / slots, rest = n % slots;
+  return full * round_ns(slots, chunk, ns_per_key, key_bytes) +
+         (rest ? round_ns(rest, chunk, ns_per_key, key_bytes) : 0.0);
+}
+// n CTAs of differing lengths: a free slot takes the next one, half a CTA is left over
+double ragged_ns(double n, int64_t slots, double chunk, double ns_per_key, double key_bytes) {
+  if (n <= slots) return round_ns(static_cast<int64_t>(n), chunk, ns_per_key, key_bytes);
+  return n / slots * round_ns(slots, chunk, ns_per_key, key_bytes) +
+         0.5 * round_ns(0, chunk, ns_per_key, key_bytes);
+}
+
+double paged_plan_tiles(const PagedShape& x, int want, int sms, PagedPlan* pl) {
+  const int rt = x.rows <= 8 ? 8 : x.rows <= 16 ? 16 : x.rows <= 32 ? 32 : 64;
+  const int ri = rt == 8 ? 0 : rt == 16 ? 1 : rt == 32 ? 2 : 3;
+  pl->rt = rt;
+  pl->row_tiles = static_cast<int>((x.rows + rt - 1) / rt);
+  const int64_t per_part = x.units * pl->row_tiles;
+  const int64_t slots = static_cast<int64_t>(sms) * (x.key_bytes > 512 ? 1 : rt == 8 ? 3 : 2);
+  auto chunk_of = [&](int64_t splits) {  // whole tiles of every kernel
+    return std::max<int64_t>(128, ((x.span + splits - 1) / splits + 127) / 128 * 128);
+  };
+  double best = 0;
+  int64_t splits = 0;
+  for (int s = want ? want : 1; s <= (want ? want : kPagedMaxSplits); s += 1 + s / 8) {
+    const int64_t chunk = chunk_of(s), parts = (x.span + chunk - 1) / chunk;
+    const double c = static_cast<double>(chunk), key = kPagedNsPerKey[x.d_index][ri];
+    // max_k bounds the lengths, which are not known here: as if half the batches
+    // were of equal sequences and half of sequences of 0.6 of it on average
+    double t = 4000. + rounds_ns(per_part * parts, slots, c, key, x.key_bytes);
+    if (x.batch > 1)
+      t = 0.5 * (t + 4000. + ragged_ns(0.6 * per_part * parts, slots, c, key, x.key_bytes));
+    if (parts > 1)
+      t += 2000. + kMergeCopies * 8. * parts * x.total_q * x.hq * x.d / kHbmBytesPerNs;
+    if (!splits || t < best) best = t, splits = parts;
+  }
+  const int64_t chunk = chunk_of(want ? want : splits);
+  pl->splits = static_cast<int>((x.span + chunk - 1) / chunk);
+  pl->chunk = static_cast<int>(chunk);
+  const size_t rows_all = static_cast<size_t>(pl->splits) * x.total_q * x.hq;
+  pl->lse_off = align256(rows_all * x.d * 4);
+  pl->bytes = pl->splits > 1 ? pl->lse_off + rows_all * 4 : 0;
+  return best;
+}
+
+// false: not open for this call
+bool paged_plan_dense(const PagedShape& x, int hkv, int sms, double limit, PagedPlan* pl) {
+  const int64_t key_rows = x.batch * (x.max_k + kGatherPad);
+  const int64_t copy = key_rows * hkv * x.d * 2;
+  if (x.rows < 64 || x.batch > 32767 || 2 * copy > kDenseBytes || key_rows >= (1 << 30))
+    return false;
+  // code read, copy written and read; two launches more
+  const double gather = 8000. + key_rows * hkv * (x.key_bytes + 8. * x.d) / kHbmBytesPerNs;
+  const int64_t tile = x.d == 256 ? 128 : 256;
+  const int64_t ctas = x.units * ((x.rows + tile - 1) / tile);
+  double best = 0;
+  int splits = 0;
+  for (int s = 1; s <= 16 && x.max_k >= 512 * s; s *= 2) {
+    double t = gather + rounds_ns(ctas * s, sms, static_cast<double>(x.span) / s,
+                                  kDenseNsPerKey[x.d_index], 0.0);
+    if (s > 1) t += 4000. + kMergeCopies * 8. * s * x.total_q * x.hq * x.d / kHbmBytesPerNs;
+    if (!splits || t < best) best = t, splits = s;
+  }
+  if (!splits || best >= limit) return false;
+  pl->dense = true;
+  pl->splits = splits;
+  pl->key_rows = key_rows;
+  pl->v_off = align256(copy);
+  pl->cu_q_off = pl->v_off + align256(copy);
+  pl->cu_k_off = pl->cu_q_off + align256((2 * static_cast<size_t>(x.batch) + 1) * 4);
+  pl->split_off = pl->cu_k_off + align256((2 * static_cast<size_t>(x.batch) + 1) * 4);
+  pl->split_bytes = splits > 1 ? attn_fwd_split_workspace_size(static_cast<int32_t>(x.total_q),
+                                                               static_cast<int32_t>(x.hq), x.d,
+                                                               splits)
+                               : 0;
+  pl->bytes = pl->split_off + pl->split_bytes;
+  return true;
+}
+
 PagedPlan paged_plan(const attn_paged_cache_t* c, int batch, int total_q, int max_q, int max_k,
                      int hq, int hi_off, int lo_off, int want, int sms) {
   PagedPlan pl{};
-  const int64_t group = hq / c->nheads_kv;
-  const int64_t rows = group * max_q;
-  pl.key_rows = static_cast<int64_t>(batch) * (static_cast<int64_t>(max_k) + kGatherPad);
-  const int64_t copy = pl.key_rows * c->nheads_kv * c->head_dim * 2;
-  pl.dense = want == 0 && rows >= kDenseRows && batch <= 32767 && 2 * copy <= kDenseBytes &&
-             pl.key_rows < (int64_t(1) << 30);
-  if (pl.dense) {
-    pl.v_off = align256(copy);
-    pl.cu_q_off = pl.v_off + align256(copy);
-    pl.cu_k_off = pl.cu_q_off + align256((2 * static_cast<size_t>(batch) + 1) * 4);
-    pl.bytes = pl.cu_k_off + align256((2 * static_cast<size_t>(batch) + 1) * 4);
-    return pl;
-  }
-  pl.nt = rows <= 8 ? 1 : 2;
-  pl.wr = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  const int rt = 8 * pl.nt * pl.wr;
-  pl.row_tiles = static_cast<int>((rows + rt - 1) / rt);
-  // keys a CTA's rows can see: with both bounds, the window and the rows' spread
-  int64_t span = max_k;
+  PagedShape x;
+  x.batch = batch;
+  x.units = static_cast<int64_t>(batch) * c->nheads_kv;
+  x.group = hq / c->nheads_kv;
+  x.rows = x.group * max_q;
+  x.max_k = max_k;
+  x.total_q = total_q;
+  x.hq = hq;
+  x.d = c->head_dim;
+  x.d_index = x.d == 64 ? 0 : x.d == 128 ? 1 : 2;
+  x.key_bytes = 2 * x.d * (c->type == ATTN_CACHE_E4M3 ? 1 : 2);
+  // keys a CTA's rows can see: with both bounds, the window and the rows' spread;
+  // parts begin at a multiple of 16
+  x.span = max_k;
   if (lo_off < kPagedNoBound && hi_off < kPagedNoBound)
-    span = std::min<int64_t>(span, static_cast<int64_t>(lo_off) + hi_off + 1 +
-                                       (rt + group - 1) / group + 1);
-  if (lo_off < kPagedNoBound) span += 15;  // parts begin at a multiple of 16
-  span = std::max<int64_t>(span, 1);
-  constexpr int bk = 128;  // parts end at a whole number of tiles of every kernel
-  const int64_t ctas = static_cast<int64_t>(batch) * c->nheads_kv * pl.row_tiles;
-  int64_t splits = want;
-  if (want == 0) {
-    splits = (4ll * sms + ctas - 1) / ctas;
-    splits = std::min<int64_t>(splits, (span + 255) / 256);
-  }
-  splits = std::max<int64_t>(1, std::min<int64_t>(splits, kPagedMaxSplits));
-  int64_t chunk = (span + splits - 1) / splits;
-  chunk = (chunk + bk - 1) / bk * bk;
-  pl.splits = static_cast<int>((span + chunk - 1) / chunk);
-  pl.chunk = static_cast<int>(chunk);
-  const size_t rows_all = static_cast<size_t>(pl.splits) * total_q * hq;
-  pl.lse_off = (rows_all * c->head_dim * 4 + 255) / 256 * 256;
-  pl.bytes = pl.splits > 1 ? pl.lse_off + rows_all * 4 : 0;
+    x.span = std::min<int64_t>(x.span, static_cast<int64_t>(lo_off) + hi_off + 2 +
+                                           (64 + x.group - 1) / x.group);
+  if (lo_off < kPagedNoBound) x.span += 15;
+  x.span = std::max<int64_t>(x.span, 1);
+  const double t = paged_plan_tiles(x, want, sms, &pl);
+  PagedPlan dense{};
+  if (want == 0 && paged_plan_dense(x, c->nheads_kv, sms, t, &dense)) return dense;
   return pl;
 }
 
@@ -274,21 +359,22 @@ attn_status_t paged_sizes(const attn_paged_cache_t* c, int32_t batch, int32_t to
   return ATTN_OK;
 }
 
-template <int D, bool FP8, int NT, int WR>
+// raises a kernel's shared memory limit once per device, launches it and, for
+// keys in parts, the merge
+template <int D, auto Kernel, int THREADS, int SMEM>
 attn_status_t launch_paged(const PagedParams& p, int batch, cudaStream_t s) {
-  using C = PagedCfg<D, FP8, NT, WR>;
-  static bool ready[kServeDevices];  // the limit has been raised on this device
+  static bool ready[kServeDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
   if (!__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE)) {
-    if (cudaFuncSetAttribute(attn_paged_kernel<D, FP8, NT, WR>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
+        cudaSuccess)
       return ATTN_ERR_CUDA;
     __atomic_store_n(&ready[dev], true, __ATOMIC_RELEASE);
   }
   const int64_t ctas = static_cast<int64_t>(batch) * p.num_splits * p.row_tiles * p.hkv;
   if (ctas > kMaxGrid) return ATTN_ERR_INVALID_ARG;
-  attn_paged_kernel<D, FP8, NT, WR><<<static_cast<unsigned>(ctas), 128, C::SMEM, s>>>(p);
+  Kernel<<<static_cast<unsigned>(ctas), THREADS, SMEM, s>>>(p);
   attn_status_t st = launched();
   if (st != ATTN_OK || p.num_splits == 1) return st;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.hq;
@@ -307,13 +393,21 @@ attn_status_t launch_paged(const PagedParams& p, int batch, cudaStream_t s) {
              : ATTN_ERR_CUDA;
 }
 
+template <int D, bool FP8, int NT, int WR>
+attn_status_t launch_tile(const PagedParams& p, int batch, cudaStream_t s) {
+  return launch_paged<D, attn_paged_kernel<D, FP8, NT, WR>, 128, PagedCfg<D, FP8, NT, WR>::SMEM>(
+      p, batch, s);
+}
+
 template <int D, bool FP8>
 attn_status_t launch_paged_rows(const PagedParams& p, const PagedPlan& pl, int batch,
                                 cudaStream_t s) {
-  if (pl.nt == 1) return launch_paged<D, FP8, 1, 1>(p, batch, s);
-  if (pl.wr == 1) return launch_paged<D, FP8, 2, 1>(p, batch, s);
-  if (pl.wr == 2) return launch_paged<D, FP8, 2, 2>(p, batch, s);
-  return launch_paged<D, FP8, 2, 4>(p, batch, s);
+  switch (pl.rt) {
+    case 8: return launch_tile<D, FP8, 1, 1>(p, batch, s);
+    case 16: return launch_tile<D, FP8, 2, 1>(p, batch, s);
+    case 32: return launch_tile<D, FP8, 2, 2>(p, batch, s);
+    default: return launch_tile<D, FP8, 2, 4>(p, batch, s);
+  }
 }
 
 }  // namespace
@@ -520,10 +614,11 @@ extern "C" attn_status_t attn_paged_fwd(
       default: st = e4m3 ? launch_gather<256, true>(g, s) : launch_gather<256, false>(g, s);
     }
     if (st != ATTN_OK) return st;
-    return attn_fwd_ex(q, g.k, g.v, g.cu_q, g.cu_k, 2 * batch, total_q,
-                       static_cast<int32_t>(pl.key_rows), max_seqlen_q, max_seqlen_k, nheads_q,
-                       cache->nheads_kv, cache->head_dim, scale, causal, window_left, window_right,
-                       softcap, return_lse, out, lse, stream);
+    return attn_fwd_split(q, g.k, g.v, g.cu_q, g.cu_k, 2 * batch, total_q,
+                          static_cast<int32_t>(pl.key_rows), max_seqlen_q, max_seqlen_k, nheads_q,
+                          cache->nheads_kv, cache->head_dim, scale, causal, window_left,
+                          window_right, softcap, pl.splits, return_lse, out, lse,
+                          ws + pl.split_off, pl.split_bytes, stream);
   }
   switch (cache->head_dim) {
     case 64:

@@ -325,6 +325,38 @@ def test_not_finite_keys_and_values(e4m3):
         assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (12, 2), (20, 2)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_not_finite_values_behind_the_mask(d, e4m3, hq, hkv, bad):
+    """A value that is not finite reaches the rows that see its key and no other
+    row of the call, whichever kernel the number of rows selects."""
+    if e4m3 and bad == math.inf:
+        return  # e4m3 has no infinity
+    page, n, lens = 32, [4, 3, 1], [90, 40, 17]
+    c = Cache(lens, lens, hkv, d, page, e4m3, seed=21, junk=math.nan)
+
+    def put(seq, pos, head, col):
+        c.v[int(c.table[seq, pos // page]), pos % page, head, col] = bad
+
+    put(0, 88, 1, 3)    # seen by the third and fourth of four rows
+    put(0, 89, 0, d - 1)  # by the last only
+    put(1, 10, 0, 7)    # under the window: by the first two of three rows
+    q = rows(sum(n), hq, d, 120, 0.2)
+    for splits in (0, 2):
+        cu = cu_of(n)
+        kc, vc, table, kw = c.to("cuda")
+        args = dict(causal=True, window=(28, -1))
+        out, lse = ea.attn_paged_fwd(q.cuda(), kc, vc, table, i32(cu), i32(lens), 4, 90,
+                                     num_splits=splits, **args, **kw)
+        ref, ref_lse, pabs = sr.attend(q, c.k, c.v, c.k_scale, c.v_scale, c.table, cu, lens,
+                                       d ** -0.5, **args)
+        got = out.cpu().double()
+        assert torch.equal(~torch.isfinite(got), ref.isnan())
+        compare(torch.where(ref.isnan(), ref, got), lse, ref, ref_lse, pabs, e4m3)
+
+
 def test_cut_off_lengths_and_bad_pages():
     # lengths past the block table are cut there; pages outside the pool read as zeros
     d, page = 128, 32
