@@ -135,7 +135,7 @@ constexpr int kRotaryThreads = 256;
 // grid: (units of all rows / 256, groups of heads_per_thread heads).  Bound by
 // HBM: every element is read once and written once.
 template <int D>
-__global__ void __launch_bounds__(kRotaryThreads) attn_rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(kRotaryThreads, 3) attn_rotary_kernel(const RotaryParams p) {
   constexpr int UNITS = D / 16;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kRotaryThreads + threadIdx.x;
   const int t = static_cast<int>(id / UNITS), c = static_cast<int>(id % UNITS);
