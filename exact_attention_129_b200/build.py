@@ -19,7 +19,7 @@ SOURCES = ["api.cu", "serve_api.cu"]
 HEADERS = ["ptx.cuh", "fwd_kernel.cuh", "fwd_pair_kernel.cuh", "bwd_kernels.cuh",
            "bwd_pair_kernel.cuh", "rotary.cuh", "paged_append.cuh", "paged_common.cuh",
            "paged_attn.cuh",
-           "paged_gather.cuh"]
+           "paged_gather.cuh", "paged_tc.cuh"]
 BINDING = os.path.join(HERE, "_serving.so")
 BINDING_SOURCE = os.path.join(CSRC, "serving_binding.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -488,6 +488,16 @@ attn_status_t bwd_launch(const BwdArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// for the kernels of serve_api.cu: the current device's error word (null if the
+// device could not be set up) and the bound of every wait
+uint32_t* device_error_word() {
+  int dev = 0;
+  DeviceState* st = device_state(&dev);
+  return st ? st->err : nullptr;
+}
+uint64_t device_wait_timeout_ns() { return wait_timeout_ns(); }
+
 }  // namespace attn
 
 using namespace attn;
@@ -814,7 +824,8 @@ extern "C" attn_status_t attn_last_device_error(attn_stream_t stream, char* msg,
                                   "bwd load", "bwd mma", "bwd softmax", "bwd dq convert",
                                   "watchdog self-test", "bwd pair load", "bwd pair mma",
                                   "bwd pair elementwise", "bwd pair exchange", "bwd pair dq",
-                                  "fwd pair load", "fwd pair mma", "fwd pair softmax"};
+                                  "fwd pair load", "fwd pair mma", "fwd pair softmax",
+                                  "paged load", "paged mma", "paged softmax"};
   const uint32_t kid = (word >> 8) & 0xff;
   char buf[128];
   std::snprintf(buf, sizeof(buf), "timed-out wait in %s (wait %u)",

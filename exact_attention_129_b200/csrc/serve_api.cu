@@ -10,9 +10,15 @@
 #include "paged_append.cuh"
 #include "paged_attn.cuh"
 #include "paged_gather.cuh"
+#include "paged_tc.cuh"
 #include "rotary.cuh"
 
 namespace attn {
+
+// api.cu
+uint32_t* device_error_word();
+uint64_t device_wait_timeout_ns();
+
 namespace {
 
 constexpr int kServeDevices = 64;
@@ -235,8 +241,8 @@ double ragged_ns(double n, int64_t slots, double chunk, double ns_per_key, doubl
 }
 
 double paged_plan_tiles(const PagedShape& x, int want, int sms, PagedPlan* pl) {
-  const int rt = x.rows <= 8 ? 8 : x.rows <= 16 ? 16 : x.rows <= 32 ? 32 : 64;
-  const int ri = rt == 8 ? 0 : rt == 16 ? 1 : rt == 32 ? 2 : 3;
+  const int rt = x.rows <= 8 ? 8 : x.rows <= 32 ? 32 : x.rows <= 64 ? 64 : 128;
+  const int ri = rt == 8 ? 0 : rt == 32 ? 1 : rt == 64 ? 2 : 3;
   pl->rt = rt;
   pl->row_tiles = static_cast<int>((x.rows + rt - 1) / rt);
   const int64_t per_part = x.units * pl->row_tiles;
@@ -362,8 +368,8 @@ attn_status_t paged_sizes(const attn_paged_cache_t* c, int32_t batch, int32_t to
 
 // raises a kernel's shared memory limit once per device, launches it and, for
 // keys in parts, the merge
-template <int D, auto Kernel, int THREADS, int SMEM>
-attn_status_t launch_paged(const PagedParams& p, int batch, cudaStream_t s) {
+template <int D, auto Kernel, int THREADS, int SMEM, class Params>
+attn_status_t launch_paged(const PagedParams& p, const Params& kp, int batch, cudaStream_t s) {
   static bool ready[kServeDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
@@ -375,7 +381,7 @@ attn_status_t launch_paged(const PagedParams& p, int batch, cudaStream_t s) {
   }
   const int64_t ctas = static_cast<int64_t>(batch) * p.num_splits * p.row_tiles * p.hkv;
   if (ctas > kMaxGrid) return ATTN_ERR_INVALID_ARG;
-  Kernel<<<static_cast<unsigned>(ctas), THREADS, SMEM, s>>>(p);
+  Kernel<<<static_cast<unsigned>(ctas), THREADS, SMEM, s>>>(kp);
   attn_status_t st = launched();
   if (st != ATTN_OK || p.num_splits == 1) return st;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.hq;
@@ -394,20 +400,24 @@ attn_status_t launch_paged(const PagedParams& p, int batch, cudaStream_t s) {
              : ATTN_ERR_CUDA;
 }
 
-template <int D, bool FP8, int NT, int WR>
-attn_status_t launch_tile(const PagedParams& p, int batch, cudaStream_t s) {
-  return launch_paged<D, attn_paged_kernel<D, FP8, NT, WR>, 128, PagedCfg<D, FP8, NT, WR>::SMEM>(
-      p, batch, s);
+template <int D, bool FP8, int KG>
+attn_status_t launch_tc(const PagedParams& p, int batch, cudaStream_t s) {
+  using C = PagedTcCfg<D, FP8, KG>;
+  const PagedTcParams tp{p, device_error_word(), device_wait_timeout_ns()};
+  if (!tp.err) return ATTN_ERR_CUDA;
+  return launch_paged<D, attn_paged_tc_kernel<D, FP8, KG>, C::THREADS, C::SMEM>(p, tp, batch, s);
 }
 
 template <int D, bool FP8>
 attn_status_t launch_paged_rows(const PagedParams& p, const PagedPlan& pl, int batch,
                                 cudaStream_t s) {
   switch (pl.rt) {
-    case 8: return launch_tile<D, FP8, 1, 1>(p, batch, s);
-    case 16: return launch_tile<D, FP8, 2, 1>(p, batch, s);
-    case 32: return launch_tile<D, FP8, 2, 2>(p, batch, s);
-    default: return launch_tile<D, FP8, 2, 4>(p, batch, s);
+    case 8:
+      return launch_paged<D, attn_paged_kernel<D, FP8, 1, 1>, 128, PagedCfg<D, FP8, 1, 1>::SMEM>(
+          p, p, batch, s);
+    case 32: return launch_tc<D, FP8, 4>(p, batch, s);
+    case 64: return launch_tc<D, FP8, 2>(p, batch, s);
+    default: return launch_tc<D, FP8, 1>(p, batch, s);
   }
 }
 

@@ -177,7 +177,8 @@ def attend(c, q, n, *, hq, splits=0, max_k=None, **mask):
     ea.attn_paged_fwd(q.cuda(), kc, vc, table, i32(cu), i32(c.lens), max(n),
                       max(c.lens) if max_k is None else max_k, num_splits=splits, out=out, lse=lse,
                       scale=scale, **mask, **kw)
-    torch.cuda.synchronize()
+    rc, msg = ea.last_device_error()
+    assert rc == 0, msg
     assert guards_intact(obuf, og) and guards_intact(lbuf, lg)
     ref, ref_lse, pabs = sr.attend(q, c.k, c.v, c.k_scale, c.v_scale, c.table, cu, c.lens, scale,
                                    **mask)
