@@ -7,9 +7,12 @@
 //   S = Q K^T  (128 rows x 64 keys),  O += P V  (128 rows x head_dim)
 //
 // Tensor memory holds Q and P as first operands, S and O: P overwrites S.  Keys and
-// values are the second operands, in shared memory as f16 (from e4m3 codes, exact)
-// or bf16, 64 keys a tile in two buffers, both as panels of 64 columns x 64 keys
-// with the 128-byte swizzle: K as a K-major, V as an MN-major operand.
+// values are the second operands in shared memory, in panels of 64 keys x 128 bytes
+// with the 128-byte swizzle, K as a K-major, V as an MN-major operand.  bf16: both as
+// they are.  e4m3: K's codes as they are (kind::f8f6f4), against Q as the sum of two
+// e4m3 rows, which holds a bf16 exactly; V converted to f16 (exact), since a weight
+// needs f16's range and bits.  (With K converted too the conversions, at 3 to 4 cycles
+// a pair and scheduler, set the pace: 44 ns a key of 512 CTAs of 32 rows.)
 //
 // The 128 rows are RT = 32, 64 or 128 query rows times KG = 4, 2 or 1 groups of
 // the tile's keys: a thread of the softmax warps owns one lane, that is one row
@@ -19,9 +22,8 @@
 // merged once at the end.  The MMAs multiply the zeros: they have the time, as
 // HBM needs 680 cycles for a tile (e4m3, head_dim 128) and the MMAs 256.
 //
-// Warps 0-3: softmax.  Warps 4-7: the loads of the next tile into registers
-// (e4m3: 16-byte pieces, converted and stored swizzled when a buffer is free; bf16:
-// cp.async straight into the buffer).  Warp 8: the MMAs.  S of tile t + 1 is
+// Warps 0-3: softmax.  Warps 4-7: the loads by cp.async (bf16: straight into one of
+// three buffers; e4m3: codes, which their thread converts into one of two buffers).  Warp 8: the MMAs.  S of tile t + 1 is
 // issued when P V of tile t is done; a tile's chain S -> softmax -> P V takes
 // about 700 cycles, and two CTAs share an SM (one at head_dim 256).
 //
@@ -57,28 +59,38 @@ struct PagedTcCfg {
   static constexpr int NC = BK / KG;         // keys per softmax thread and tile
   static constexpr int THREADS = 288;
   static constexpr int PANEL = BK * 128;     // 64 keys x 64 columns of 2 bytes
-  static constexpr int TILE = PANEL * (D / 64);  // K or V of a tile
-  static constexpr int BUFFER = 2 * TILE;
+  static constexpr int TILE = PANEL * (D / 64);  // V of a tile, or K in bf16
+  // bf16: three buffers of K and V.  e4m3: two of V in f16, RAW tiles of V's codes on
+  // their way, and K's codes in a ring that holds those and the two in use
+  static constexpr int NBUF = FP8 ? 2 : 3;
+  static constexpr int RAW = FP8 ? (D == 64 ? 4 : 2) : 0;
+  static constexpr int RAW_TILE = FP8 ? BK * D + 32 : 0;  // codes of V, scales
+  static constexpr int NK = FP8 ? RAW + 2 : NBUF;
+  static constexpr int K_TILE = FP8 ? PANEL * (D > 128 ? 2 : 1) : TILE;  // 128 codes a row
+  static constexpr int V_OFF = NK * K_TILE;
+  static constexpr int RAW_OFF = V_OFF + NBUF * TILE;
+  static constexpr int TILES_END = RAW_OFF + RAW * RAW_TILE;
   static constexpr int Q_COL = 64, O_COL = 64 + D / 2;  // S at column 0
   static constexpr int TMEM_COLS = D == 256 ? 512 : 256;
   static constexpr int CTAS = D == 256 || KG == 1 ? 1 : 2;  // (64 keys a thread need registers)
-  // poison bits of a tile's values: [2 signs][64 keys][D / 32], for two buffers, and
-  // what each of the 128 lanes has seen
+  // bits of a tile's values that are not finite, [NBUF][2 signs][64 keys][D / 32], and
+  // of what each of the 128 lanes has seen
   static constexpr int WORDS = D / 32;
   static constexpr int STAGE_ROW = 68;       // floats: a chunk of 64 columns of O at the end
   static constexpr int STAGE = 128 * STAGE_ROW * 4;
-  static constexpr int BAR_OFF = 2 * BUFFER > STAGE ? 2 * BUFFER : STAGE;
-  static constexpr int SCALE_OFF = BAR_OFF + 128;              // [2][4] float2
-  static constexpr int FLAG_OFF = SCALE_OFF + 64;              // [2] ints, abort, tmem
+  static constexpr int BAR_OFF = TILES_END > STAGE ? TILES_END : STAGE;
+  static constexpr int SCALE_OFF = BAR_OFF + 128;              // [NBUF][4] float2
+  static constexpr int FLAG_OFF = SCALE_OFF + NBUF * 32;       // [NBUF] ints, abort, tmem
   static constexpr int ML_OFF = FLAG_OFF + 32;                 // [128] m, l
-  static constexpr int BAD_OFF = ML_OFF + 128 * 8;             // [2][2][64][WORDS]
-  static constexpr int SEEN_OFF = BAD_OFF + 2 * 2 * 64 * WORDS * 4;  // [2][128][WORDS]
+  static constexpr int BAD_OFF = ML_OFF + 128 * 8;             // [NBUF][2][64][WORDS]
+  static constexpr int SEEN_OFF = BAD_OFF + NBUF * 2 * 64 * WORDS * 4;  // [2][128][WORDS]
   static constexpr int USED = SEEN_OFF + 2 * 128 * WORDS * 4 + 1024;  // 1024-byte alignment
   // no third CTA on an SM: it would wait for tensor memory
   static constexpr int SMEM = USED > 80 * 1024 ? USED : 80 * 1024;
   static constexpr float OFFSET = FP8 ? 6.f : 0.f;
   static constexpr float RAISE = 8.f + OFFSET;
   static constexpr uint32_t FORMAT = FP8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // f16: zeros
+  // e4m3: S by kind::f8f6f4, whose formats are all 0 for e4m3
   static constexpr uint32_t IDESC_S = idesc_bf16(128, BK, false, false) & FORMAT;
   static constexpr uint32_t IDESC_O = idesc_bf16(128, D, false, true) & FORMAT;
 };
@@ -92,6 +104,18 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
                : "memory");
+}
+
+// tcgen05.mma kind::f8f6f4, A (e4m3, four to a column) from tensor memory, B from shared
+// memory, fp32 accumulation; executed like mma_ts
+__device__ __forceinline__ void mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // 2-byte values of a 16-byte chunk that are not finite: bits of columns (as +inf, -inf, both for
@@ -116,7 +140,7 @@ template <int D, bool FP8, int KG>
 __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
     attn_paged_tc_kernel(const PagedTcParams tp) {
   using C = PagedTcCfg<D, FP8, KG>;
-  constexpr int BK = C::BK, RT = C::RT, NC = C::NC, WORDS = C::WORDS;
+  constexpr int BK = C::BK, RT = C::RT, NC = C::NC, WORDS = C::WORDS, NBUF = C::NBUF;
   const PagedParams& p = tp.a;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -129,14 +153,14 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
   const int rows = w.rows, kb = w.kb, ke = w.ke;
   const int tiles = (ke - kb + BK - 1) / BK;
 
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // [2] a buffer is written
-  uint64_t* empty = full + 2;                                       // [2] its P V is done
-  uint64_t* s_full = full + 4;
-  uint64_t* p_full = full + 5;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // [NBUF] it is written
+  uint64_t* empty = full + NBUF;                                    // [NBUF] its P V is done
+  uint64_t* s_full = full + 2 * NBUF;
+  uint64_t* p_full = full + 2 * NBUF + 1;
   float2* scales = reinterpret_cast<float2*>(smem + C::SCALE_OFF);
-  int* tile_bad = reinterpret_cast<int*>(smem + C::FLAG_OFF);       // [2]
-  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF + 8);
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::FLAG_OFF + 12);
+  int* tile_bad = reinterpret_cast<int*>(smem + C::FLAG_OFF);       // [NBUF]
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF + 16);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::FLAG_OFF + 20);
   float2* ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + C::BAD_OFF);
   uint32_t* seen = reinterpret_cast<uint32_t*>(smem + C::SEEN_OFF);
@@ -146,7 +170,7 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NBUF; ++i) {
       mbar_init(&full[i], 128);
       mbar_init(&empty[i], 1);
       tile_bad[i] = 0;
@@ -175,8 +199,9 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
       const bool live = r < rows;
       const uint4* src =
           reinterpret_cast<const uint4*>(p.q + w.row_index(p, live ? r : 0) * D);
-      float up = 1.f;
       if constexpr (FP8) {
+        // scaled so that the largest element is in [2^7, 2^8), and as a sum of two codes:
+        // 4 significant bits, then the rest; exact for elements down to 2^-10 of that
         uint32_t m = 0;
 #pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {
@@ -185,25 +210,46 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
           const uint32_t v = __vmaxu2(__vmaxu2(x.x & M, x.y & M), __vmaxu2(x.z & M, x.w & M));
           m = max(m, max(v & 0xffffu, v >> 16));
         }
-        const int e = m >= 0x7f80u ? 14 : max(static_cast<int>(m >> 7) - 127, -100);
-        up = exp2_int(14 - e);
-        f_row *= exp2_int(e - 14);
-      }
+        const int e = m >= 0x7f80u ? 7 : max(static_cast<int>(m >> 7) - 127, -100);
+        const float up = exp2_int(7 - e);
+        f_row *= exp2_int(e - 7);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {  // 16 columns of tensor memory: 32 elements
-        uint32_t q[16];
+        for (int c = 0; c < D / 32; ++c) {  // 32 elements: 8 columns of each part
+          uint32_t hi8[8], lo8[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 x = src[c * 4 + i];
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+          for (int i = 0; i < 4; ++i) {
+            const uint4 x = src[c * 4 + i];
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t v = y[k];
-            if constexpr (FP8) v = pg_f16_pair(bf16_lo(v) * up, bf16_hi(v) * up);
-            q[4 * i + k] = live ? v : 0u;
+            for (int k = 0; k < 2; ++k) {
+              const float v[4] = {bf16_lo(y[2 * k]) * up, bf16_hi(y[2 * k]) * up,
+                                  bf16_lo(y[2 * k + 1]) * up, bf16_hi(y[2 * k + 1]) * up};
+              const uint32_t h = e4m3_pair(v[0], v[1]) | (e4m3_pair(v[2], v[3]) << 16);
+              const uint32_t h01 = pg_f16_lo(h), h23 = pg_f16_hi(h);
+              const uint32_t g =
+                  e4m3_pair(v[0] - pg_weight<true>(h01), v[1] - pg_weight<true>(h01 >> 16)) |
+                  (e4m3_pair(v[2] - pg_weight<true>(h23), v[3] - pg_weight<true>(h23 >> 16)) << 16);
+              hi8[2 * i + k] = live ? h : 0u;
+              lo8[2 * i + k] = live ? g : 0u;
+            }
           }
+          tmem_st8(lanes + C::Q_COL + c * 8, hi8);
+          tmem_st8(lanes + C::Q_COL + D / 4 + c * 8, lo8);
         }
-        tmem_st16(lanes + C::Q_COL + c * 16, q);
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {  // 16 columns of tensor memory: 32 elements
+          uint32_t q[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 x = src[c * 4 + i];
+            q[4 * i] = live ? x.x : 0u;
+            q[4 * i + 1] = live ? x.y : 0u;
+            q[4 * i + 2] = live ? x.z : 0u;
+            q[4 * i + 3] = live ? x.w : 0u;
+          }
+          tmem_st16(lanes + C::Q_COL + c * 16, q);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -217,8 +263,8 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
     bool poisoned = false;
     bool ok = true;
     for (int t = 0; t < tiles; ++t) {
-      const int b = t & 1;
-      if (!mbar_wait(&full[b], (t >> 1) & 1, abort, tp.err, ERR_PAGED_SOFTMAX | 1,
+      const int b = t % NBUF;
+      if (!mbar_wait(&full[b], (t / NBUF) & 1, abort, tp.err, ERR_PAGED_SOFTMAX | 1,
                      tp.timeout_ns) ||
           !mbar_wait(s_full, t & 1, abort, tp.err, ERR_PAGED_SOFTMAX | 2, tp.timeout_ns))
         ok = false;
@@ -337,7 +383,7 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
       mbar_arrive(p_full);
     }
     const int last = tiles - 1;
-    if (ok) ok = mbar_wait(&empty[last & 1], (last >> 1) & 1, abort, tp.err,
+    if (ok) ok = mbar_wait(&empty[last % NBUF], (last / NBUF) & 1, abort, tp.err,
                            ERR_PAGED_SOFTMAX | 3, tp.timeout_ns);
     // O of the groups of a row, merged: in chunks of 64 columns through shared memory
     // (the buffers are free)
@@ -464,102 +510,104 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
       return (plus | minus) != 0;
     };
     auto wait_empty = [&](int t) {
-      bool ok = t < 2 || mbar_wait(&empty[t & 1], ((t >> 1) + 1) & 1, abort, tp.err,
+      bool ok = t < NBUF || mbar_wait(&empty[t % NBUF], ((t / NBUF) + 1) & 1, abort, tp.err,
                                    ERR_PAGED_LOAD | 1, tp.timeout_ns);
       return __all_sync(0xffffffffu, ok) != 0;
     };
     if constexpr (FP8) {
-      uint4 kx[N], vx[N];
-      float sx = 0.f;
-      auto load = [&](int t) {
+      // A thread converts the codes that it loaded itself, so it waits for its own
+      // copies only; they lie [piece][thread], every access in different banks.
+      const uint32_t mine = sbase + C::RAW_OFF + lt * 16;
+      auto issue = [&](int t) {
+        const uint32_t st = mine + (t % C::RAW) * C::RAW_TILE;
+        const uint32_t kd = sbase + (t % C::NK) * C::K_TILE + (piece >> 3) * C::PANEL;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           uint64_t ko, vo;
           const bool live = source(t, i, &ko, &vo);
-          kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
-          if (live) {
-            kx[i] = __ldg(reinterpret_cast<const uint4*>(kbase + ko));
-            vx[i] = __ldg(reinterpret_cast<const uint4*>(vbase + vo));
-          }
+          pg_cp16(kd + tc_chunk(row0 + i * STEP, piece & 7), kbase + ko, live);
+          pg_cp16(st + i * 2048, vbase + vo, live);
         }
-        sx = 0.f;
         if (lt < 8) {  // scales of the tile's four 16-key blocks
           const int key = kb + t * BK + (lt >> 1) * 16;
           const uint32_t pg = __ldg(table + min(key >> p.page_shift, last_entry));
-          if (key < ke && pg < static_cast<uint32_t>(p.num_pages))
-            sx = __ldg(((lt & 1) ? p.vc.scale : p.kc.scale) + static_cast<int64_t>(pg) * p.hkv +
-                       w.h);
+          const bool live = key < ke && pg < static_cast<uint32_t>(p.num_pages);
+          pg_cp4(sbase + C::RAW_OFF + (t % C::RAW) * C::RAW_TILE + BK * D + lt * 4,
+                 ((lt & 1) ? p.vc.scale : p.kc.scale) +
+                     static_cast<int64_t>(live ? pg : 0u) * p.hkv + w.h,
+                 live);
         }
       };
       find_pages(0);
-      load(0);
-      if (tiles > 1) find_pages(1);
+#pragma unroll 1
+      for (int t = 0; t < C::RAW; ++t) {
+        if (t < tiles) issue(t);
+        pg_commit();
+        find_pages(t + 1);  // (past the last tile: the last entry again)
+      }
       for (int t = 0; t < tiles; ++t) {
-        const int b = t & 1;
+        const int b = t % NBUF;
+        pg_wait<C::RAW - 1>();
         if (!wait_empty(t)) break;
         const bool mix = mixed(t);
         if (mix) clear_bad(b);
-        const uint32_t kd = sbase + b * C::BUFFER + (piece >> 2) * C::PANEL, vd = kd + C::TILE;
-        const int c0 = 2 * (piece & 3), swap = (piece >> 2) & 1;  // the halves of a phase's lanes
+        const uint8_t* codes = smem + C::RAW_OFF + (t % C::RAW) * C::RAW_TILE;
+        const uint32_t vd = sbase + C::V_OFF + b * C::TILE + (piece >> 2) * C::PANEL;
+        // the two chunks of a piece; the lanes of an odd panel take them in the other
+        // order, so that the 8 lanes of a store lie in different banks
+        const int swap = (piece >> 2) & 1, c0 = 2 * (piece & 3) + swap;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int key = row0 + i * STEP;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint4 x = kv ? vx[i] : kx[i];
-            uint32_t lo4[4] = {pg_f16_lo(x.x), pg_f16_hi(x.x), pg_f16_lo(x.y), pg_f16_hi(x.y)};
-            uint32_t hi4[4] = {pg_f16_lo(x.z), pg_f16_hi(x.z), pg_f16_lo(x.w), pg_f16_hi(x.w)};
-            if (kv && mix) {
-              clean(b, key, piece * 16, lo4);
-              clean(b, key, piece * 16 + 8, hi4);
-            }
-            const uint32_t dst = kv ? vd : kd;
-            // lanes of one panel begin with the chunk the other panel's end with: the 8
-            // lanes of a store lie in different banks
-            st_shared16(dst + tc_chunk(key, c0 + swap), swap ? hi4[0] : lo4[0],
-                        swap ? hi4[1] : lo4[1], swap ? hi4[2] : lo4[2], swap ? hi4[3] : lo4[3]);
-            st_shared16(dst + tc_chunk(key, c0 + 1 - swap), swap ? lo4[0] : hi4[0],
-                        swap ? lo4[1] : hi4[1], swap ? lo4[2] : hi4[2], swap ? lo4[3] : hi4[3]);
+          const uint4 x = *reinterpret_cast<const uint4*>(codes + i * 2048 + lt * 16);
+          const uint32_t w0 = swap ? x.z : x.x, w1 = swap ? x.w : x.y;
+          const uint32_t w2 = swap ? x.x : x.z, w3 = swap ? x.y : x.w;
+          uint32_t first[4] = {pg_f16_lo(w0), pg_f16_hi(w0), pg_f16_lo(w1), pg_f16_hi(w1)};
+          uint32_t second[4] = {pg_f16_lo(w2), pg_f16_hi(w2), pg_f16_lo(w3), pg_f16_hi(w3)};
+          if (mix) {
+            clean(b, key, piece * 16 + 8 * swap, first);
+            clean(b, key, piece * 16 + 8 - 8 * swap, second);
           }
+          st_shared16(vd + tc_chunk(key, c0), first[0], first[1], first[2], first[3]);
+          st_shared16(vd + tc_chunk(key, c0 ^ 1), second[0], second[1], second[2], second[3]);
         }
-        if (lt < 8) reinterpret_cast<float*>(scales + b * 4)[lt] = sx;
+        if (lt < 8)
+          reinterpret_cast<float*>(scales + b * 4)[lt] =
+              reinterpret_cast<const float*>(codes + BK * D)[lt];
         fence_async_smem();
         mbar_arrive(&full[b]);
-        if (t + 1 < tiles) {
-          load(t + 1);
-          if (t + 2 < tiles) find_pages(t + 2);
-        }
+        if (t + C::RAW < tiles) issue(t + C::RAW);
+        pg_commit();
+        find_pages(t + C::RAW + 1);
       }
+      pg_wait<0>();
     } else {
-      // tile t + 1 is on its way while tile t is handed over
+      // two tiles are on their way while one is handed over and used
       auto issue = [&](int t) {
-        const int b = t & 1;
-        const uint32_t kd = sbase + b * C::BUFFER + (piece >> 3) * C::PANEL;
+        const int b = t % NBUF;
+        const uint32_t kd = sbase + b * C::TILE + (piece >> 3) * C::PANEL;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           uint64_t ko, vo;
           const bool live = source(t, i, &ko, &vo);
           const uint32_t o = tc_chunk(row0 + i * STEP, piece & 7);
           pg_cp16(kd + o, kbase + ko, live);
-          pg_cp16(kd + C::TILE + o, vbase + vo, live);
+          pg_cp16(kd + C::V_OFF + o, vbase + vo, live);
         }
       };
       find_pages(0);
-      issue(0);
-      pg_commit();
-      if (tiles > 1) find_pages(1);
-      for (int t = 0; t < tiles; ++t) {
-        const int b = t & 1;
-        if (t + 1 < tiles) {
-          if (!wait_empty(t + 1)) break;
-          issue(t + 1);
-          if (t + 2 < tiles) find_pages(t + 2);
-        }
+#pragma unroll 1
+      for (int t = 0; t < NBUF - 1; ++t) {
+        if (t < tiles) issue(t);
         pg_commit();
-        pg_wait<1>();
+        find_pages(t + 1);
+      }
+      for (int t = 0; t < tiles; ++t) {
+        const int b = t % NBUF;
+        pg_wait<NBUF - 2>();
         if (mixed(t)) {
           clear_bad(b);
-          const uint32_t vd = sbase + b * C::BUFFER + C::TILE + (piece >> 3) * C::PANEL;
+          const uint32_t vd = sbase + C::V_OFF + b * C::TILE + (piece >> 3) * C::PANEL;
           for (int i = 0; i < N; ++i) {
             const int key = row0 + i * STEP;
             uint4* at = reinterpret_cast<uint4*>(smem + (vd - sbase) + tc_chunk(key, piece & 7));
@@ -570,6 +618,12 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
         }
         fence_async_smem();
         mbar_arrive(&full[b]);
+        if (t + NBUF - 1 < tiles) {
+          if (!wait_empty(t + NBUF - 1)) break;
+          issue(t + NBUF - 1);
+        }
+        pg_commit();
+        find_pages(t + NBUF);
       }
       pg_wait<0>();
     }
@@ -578,28 +632,38 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
     named_bar_sync(1, 160);
     tc_fence_after();
     const uint64_t kdesc = sdesc_sw128(sbase, 16, 1024);
-    const uint64_t vdesc = sdesc_sw128(sbase + C::TILE, C::PANEL, 1024);
+    const uint64_t vdesc = sdesc_sw128(sbase + C::V_OFF, C::PANEL, 1024);
     for (int t = 0; t < tiles; ++t) {
-      const int b = t & 1;
-      const uint64_t off = static_cast<uint64_t>(b) * (C::BUFFER >> 4);
+      const int b = t % NBUF;
+      const uint64_t kt = kdesc + static_cast<uint64_t>(t % C::NK) * (C::K_TILE >> 4);
+      const uint64_t vt = vdesc + static_cast<uint64_t>(b) * (C::TILE >> 4);
       // the tile is there; S is free: P V of the tile before has read P
-      if (!mbar_wait_warp(&full[b], (t >> 1) & 1, abort, tp.err, ERR_PAGED_MMA | 1,
+      if (!mbar_wait_warp(&full[b], (t / NBUF) & 1, abort, tp.err, ERR_PAGED_MMA | 1,
                           tp.timeout_ns))
         break;
-      if (t > 0 && !mbar_wait_warp(&empty[b ^ 1], ((t - 1) >> 1) & 1, abort, tp.err,
+      if (t > 0 && !mbar_wait_warp(&empty[(t - 1) % NBUF], ((t - 1) / NBUF) & 1, abort, tp.err,
                                    ERR_PAGED_MMA | 2, tp.timeout_ns))
         break;
       tc_fence_after();
+      if constexpr (FP8) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_ts(tmem, tmem + C::Q_COL + k * 8,
-               kdesc + off + (k >> 2) * (C::PANEL >> 4) + (k & 3) * 2, C::IDESC_S, k != 0);
+        for (int k = 0; k < 2 * (D / 32); ++k) {  // both parts of Q, 32 columns of the head each
+          const int c = k % (D / 32);
+          mma_ts_f8(tmem, tmem + C::Q_COL + k * 8, kt + (c >> 2) * (C::PANEL >> 4) + (c & 3) * 2,
+                    C::IDESC_S, k != 0);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ts(tmem, tmem + C::Q_COL + k * 8, kt + (k >> 2) * (C::PANEL >> 4) + (k & 3) * 2,
+                 C::IDESC_S, k != 0);
+      }
       mma_commit(s_full);
       if (!mbar_wait_warp(p_full, t & 1, abort, tp.err, ERR_PAGED_MMA | 3, tp.timeout_ns)) break;
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < BK / 16; ++k)
-        mma_ts(tmem + C::O_COL, tmem + k * 8, vdesc + off + k * (16 * 128 >> 4), C::IDESC_O,
+        mma_ts(tmem + C::O_COL, tmem + k * 8, vt + k * (16 * 128 >> 4), C::IDESC_O,
                (t | k) != 0);
       mma_commit(&empty[b]);
     }
