@@ -490,13 +490,14 @@ attn_status_t bwd_launch(const BwdArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // for the kernels of serve_api.cu: the current device's error word (null if the
-// device could not be set up) and the bound of every wait
+// device could not be set up), the bound of every wait, cuTensorMapEncodeTiled
 uint32_t* device_error_word() {
   int dev = 0;
   DeviceState* st = device_state(&dev);
   return st ? st->err : nullptr;
 }
 uint64_t device_wait_timeout_ns() { return wait_timeout_ns(); }
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
 
 }  // namespace attn
 

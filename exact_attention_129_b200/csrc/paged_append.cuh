@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(128) attn_append_few_kernel(const AppendParams
 // kv_groups + query head groups)
 // (two CTAs an SM instead of one at 79 registers: 104 -> 78 us for 16384 tokens)
 template <int D, bool E4M3, int IPT>
-__global__ void __launch_bounds__(512, IPT == 1 ? 2 : 1) attn_append_page_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(512, IPT == 1 ? 2 : 1)
+    attn_append_page_kernel(const AppendParams p) {
   constexpr int L = D / 16;
   __shared__ uint32_t amax[3][2];  // [head modulo 3][K, V]
   const int b = static_cast<int>(blockIdx.x / p.page_bound);

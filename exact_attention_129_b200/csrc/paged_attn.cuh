@@ -1,12 +1,12 @@
 // paged_attn.cuh -- attention of up to 8 query rows of a group per sequence (a
-// decoding step, or a few rows of a small group) over a paged key/value cache in
-// bf16 or e4m3 (one scale per page and key/value head).
+// decoding step, or a few rows of a small group), 16 in e4m3, over a paged key/value
+// cache in bf16 or e4m3 (one scale per page and key/value head).
 //
 //   x_j = log2(e) scale (q . Kcode_j) kscale_j        (then softcap and mask)
 //   l = sum_j 2^(x_j - m),   O = sum_j 2^(x_j - m) vscale_j Vcode_j / l
 //
-// Bound by HBM: each code is read once and does 8 multiply-adds, far under the
-// tensor cores' ridge.  So the design feeds the loads: cp.async fills tiles of
+// Bound by HBM for up to 8 rows: each code is read once and does 8 multiply-adds, far
+// under the tensor cores' ridge.  So the design feeds the loads: cp.async fills tiles of
 // 64 or 128 keys, and two or three CTAs share an SM.
 //
 // The products run transposed, on mma.m16n8k16: S^T = K Q^T with 16 keys as the
@@ -40,13 +40,13 @@
 
 namespace attn {
 
-template <int D, bool FP8, int NT, int WR>
+template <int D, bool FP8, int NT>
 struct PagedCfg {
   static constexpr int ESZ = FP8 ? 1 : 2;
   static constexpr int ROWB = D * ESZ;       // bytes of a cached row
   static constexpr int CPR = ROWB / 16;      // 16-byte pieces of it
   static constexpr int THREADS = 128;
-  static constexpr int WK = 4 / WR;          // warps along a tile's keys
+  static constexpr int WK = 4;               // warps, along a tile's keys
   // Tiles and stages measured on 16 sequences of 64K (e4m3, head_dim 128): 128
   // keys x 2 stages 351 us, 128 x 3 382, 64 x 4 381: a third CTA on an SM (64 KB
   // each) beats deeper stages.  Rows of 256 bytes: 64 x 2 334 us against 64 x 3
@@ -58,7 +58,7 @@ struct PagedCfg {
   // faster with one), all of up to 4 for more
   static constexpr int KT_MOST = NT > 1 ? 4 : ROWB == 64 ? 1 : 2;
   static constexpr int KT = KW < KT_MOST ? KW : KT_MOST;
-  static constexpr int RT = 8 * NT * WR;     // query rows per CTA
+  static constexpr int RT = 8 * NT;          // query rows per CTA
   static constexpr int TILE = BK * ROWB;
   static constexpr int STAGES = ROWB == 64 ? 3 : 2;
   static constexpr int STAGE = 2 * TILE + 2 * (BK / 16) * 4;  // K, V, their scales
@@ -82,14 +82,14 @@ struct PagedCfg {
   static constexpr float RAISE = 8.f + OFFSET;  // above m by this, m is raised
 };
 
-template <int D, bool FP8, int NT, int WR>
-__global__ void __launch_bounds__(128, PagedCfg<D, FP8, NT, WR>::CTAS) attn_paged_kernel(const PagedParams p) {
-  using C = PagedCfg<D, FP8, NT, WR>;
+template <int D, bool FP8, int NT>
+__global__ void __launch_bounds__(128, PagedCfg<D, FP8, NT>::CTAS)
+    attn_paged_kernel(const PagedParams p) {
+  using C = PagedCfg<D, FP8, NT>;
   constexpr int BK = C::BK, KT = C::KT, WK = C::WK, RT = C::RT, CPR = C::CPR;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wk = warp % WK, wr = warp / WK;
   const int quad = lane & 3, oct = lane >> 2;
   const int mat = lane >> 3, in8 = lane & 7;
 
@@ -115,8 +115,7 @@ __global__ void __launch_bounds__(128, PagedCfg<D, FP8, NT, WR>::CTAS) attn_page
     row_hi[tid] = w.row_hi(p, i);
   }
   __syncthreads();
-  const int rb = wr * 8 * NT;  // the warp's first row
-  const uint16_t* q_row = qs + (rb + oct) * C::QROW;
+  const uint16_t* q_row = qs + oct * C::QROW;
   uint32_t qf[C::QREG ? NT : 1][C::QREG ? D / 16 : 1][2];
   if constexpr (C::QREG) {
 #pragma unroll
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(128, PagedCfg<D, FP8, NT, WR>::CTAS) attn_page
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      rf[nt][j] = fac[rb + nt * 8 + 2 * quad + j];
+      rf[nt][j] = fac[nt * 8 + 2 * quad + j];
       m[nt][j] = -INFINITY;
       l[nt][j] = 0.f;
     }
@@ -163,7 +162,7 @@ __global__ void __launch_bounds__(128, PagedCfg<D, FP8, NT, WR>::CTAS) attn_page
     const float2* scales = reinterpret_cast<const float2*>(stage + 2 * C::TILE) ;
 #pragma unroll 1
     for (int step = 0; step < C::KW / KT; ++step) {
-      const int kr0 = (wk * C::KW + step * KT) * 16;  // the warp's rows of the tile
+      const int kr0 = (warp * C::KW + step * KT) * 16;  // the warp's rows of the tile
       const int key0 = kb + t * BK + kr0;
       if (key0 >= ke) break;  // the sequence ends before them
 
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(128, PagedCfg<D, FP8, NT, WR>::CTAS) attn_page
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int key = k0 + oct + (x >> 1) * 8, r = rb + nt * 8 + 2 * quad + (x & 1);
+              const int key = k0 + oct + (x >> 1) * 8, r = nt * 8 + 2 * quad + (x & 1);
               if (key < row_lo[r] || key > row_hi[r] || key >= ke) s[kt][nt][x] = -INFINITY;
             }
         }
@@ -324,7 +323,7 @@ __global__ void __launch_bounds__(128, PagedCfg<D, FP8, NT, WR>::CTAS) attn_page
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                  const int r = rb + nt * 8 + 2 * quad + j;
+                  const int r = nt * 8 + 2 * quad + j;
                   const uint32_t pair =
                       __shfl_sync(0xffffffffu, k < 8 ? pf[kt][nt][0] : pf[kt][nt][1],
                                   (2 * quad + j) * 4 + (k & 7) / 2);
@@ -401,15 +400,14 @@ __global__ void __launch_bounds__(128, PagedCfg<D, FP8, NT, WR>::CTAS) attn_page
   constexpr int V4 = D / 4;
   for (int x = tid; x < rows * V4; x += 128) {
     const int r = x / V4, c = (x % V4) * 4;
-    const int src = (r / (8 * NT)) * WK * 8 * NT + r % (8 * NT);  // row in the first warp's part
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < WK; ++i) top = fmaxf(top, ml[2 * (src + i * 8 * NT)]);
+    for (int i = 0; i < WK; ++i) top = fmaxf(top, ml[2 * (r + i * 8 * NT)]);
     const float base = top == -INFINITY ? 0.f : top;
     float sum = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
 #pragma unroll
     for (int i = 0; i < WK; ++i) {
-      const int q = src + i * 8 * NT;
+      const int q = r + i * 8 * NT;
       const float f = pg_ex2(ml[2 * q] - base);
       const float4 v = *reinterpret_cast<const float4*>(ob + q * C::OROW + c);
       sum += f * ml[2 * q + 1];

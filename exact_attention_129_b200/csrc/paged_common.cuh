@@ -140,7 +140,7 @@ struct PagedPlace {
   int nk, delta;
   int klo, khi;               // keys [klo, khi) are seen by some row,
   int in_lo, in_hi;           // [in_lo, in_hi) by every row
-  int kb, ke;                 // this part: [kb, ke), kb a multiple of 16
+  int kb, ke;                 // this part: [kb, ke)
   int64_t row_base;
 
   __device__ int row_hi(const PagedParams& p, int i) const {
@@ -159,8 +159,9 @@ struct PagedPlace {
     const int64_t t = g / p.hq;
     p.lse[(g - t * p.hq) * static_cast<int64_t>(p.total_q) + t] = l2 * 0.6931471805599453f;
   }
-  // false: the CTA has no rows or no keys (its outputs are then written here)
-  template <int D, int RT, int THREADS>
+  // false: the CTA has no rows or no keys (its outputs are then written here); parts
+  // begin at multiples of ALIGN
+  template <int D, int RT, int THREADS, int ALIGN = 16>
   __device__ bool find(const PagedParams& p) {
     const int tid = threadIdx.x;
     // heads fastest: CTAs that run together read neighbouring rows of a token-major pool
@@ -184,7 +185,8 @@ struct PagedPlace {
     khi = row_hi(p, i_last) + 1;
     in_lo = row_lo(p, i_last);
     in_hi = row_hi(p, i_first) + 1;
-    const int64_t kb64 = static_cast<int64_t>(klo & ~15) + static_cast<int64_t>(split) * p.chunk;
+    const int64_t kb64 =
+        static_cast<int64_t>(klo & ~(ALIGN - 1)) + static_cast<int64_t>(split) * p.chunk;
     ke = khi;
     if (split + 1 < p.num_splits && kb64 + p.chunk < khi) ke = static_cast<int>(kb64 + p.chunk);
     row_base = static_cast<int64_t>(c0) * p.hq + static_cast<int64_t>(h) * p.group;
@@ -221,8 +223,8 @@ __device__ __forceinline__ uint32_t pg_swizzle(int row, int c) {
 
 // Asynchronous loads of tile t (BK keys from kb on) into its stage: K, V, for e4m3
 // the scales of its 16-key blocks.  The pages of the blocks come through shared
-// memory some tiles ahead, so that no load waits for the block table.  Addresses are 32-bit products of a
-// page or slot with a stride, added to 64-bit bases.
+// memory some tiles ahead, so that no load waits for the block table.  Addresses are
+// 32-bit products of a page or slot with a stride, added to 64-bit bases.
 template <class C>
 struct PagedLoader {
   static constexpr int COPIES = C::BK * C::CPR / C::THREADS;

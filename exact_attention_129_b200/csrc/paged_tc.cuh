@@ -1,31 +1,39 @@
-// paged_tc.cuh -- attention over a paged cache for 9 to 128 query rows of a group
-// per CTA, on the tensor cores' tcgen05 path: drafts being verified, short chunks,
-// wide groups.  The mma.sync kernel of paged_attn.cuh is bound by its matrix
-// instructions and conversions there (16 rows 1.6, 64 rows 4 times the time HBM
+// paged_tc.cuh -- attention over a paged cache for 9 (e4m3: 17) to 128 query rows of a
+// group per CTA, on the tensor cores' tcgen05 path: drafts being verified, short
+// chunks, wide groups.  The mma.sync kernel of paged_attn.cuh is bound by its matrix
+// instructions and conversions there (32 rows 1.6 and 64 rows 4 times the time HBM
 // needs for an e4m3 cache of head_dim 128).
 //
-//   S = Q K^T  (128 rows x 64 keys),  O += P V  (128 rows x head_dim)
+//   S = Q K^T  (128 rows x 64 or 128 keys),  O += P V  (128 rows x head_dim)
 //
 // Tensor memory holds Q and P as first operands, S and O: P overwrites S.  Keys and
-// values are the second operands in shared memory, in panels of 64 keys x 128 bytes
-// with the 128-byte swizzle, K as a K-major, V as an MN-major operand.  bf16: both as
-// they are.  e4m3: K's codes as they are (kind::f8f6f4), against Q as the sum of two
-// e4m3 rows, which holds a bf16 exactly; V converted to f16 (exact), since a weight
-// needs f16's range and bits.  (With K converted too the conversions, at 3 to 4 cycles
-// a pair and scheduler, set the pace: 44 ns a key of 512 CTAs of 32 rows.)
+// values are the second operands in shared memory, in swizzled panels (K of 64 or 128
+// bytes a key, K-major; V of 64 columns, MN-major).  bf16: both as they are.  e4m3: K's
+// codes as they are (kind::f8f6f4), against Q as the sum of two e4m3 rows, which holds
+// a bf16 exactly; V converted to f16 (exact), since a weight needs f16's range and
+// bits.  (With K converted too the conversions, at 3 to 4 cycles a pair and scheduler,
+// set the pace.)
 //
 // The 128 rows are RT = 32, 64 or 128 query rows times KG = 4, 2 or 1 groups of
 // the tile's keys: a thread of the softmax warps owns one lane, that is one row
-// and 16, 32 or 64 of the 64 keys, with an m, l and O of its own; it writes zeros
+// and BK / KG of the tile's BK keys, with an m, l and O of its own; it writes zeros
 // as the weights of the other keys.  So the softmax needs no exchange between
 // threads, all four warps work for few rows too, and the groups' parts are
-// merged once at the end.  The MMAs multiply the zeros: they have the time, as
-// HBM needs 680 cycles for a tile (e4m3, head_dim 128) and the MMAs 256.
+// merged once at the end.  The MMAs multiply the zeros; they have the time.
 //
-// Warps 0-3: softmax.  Warps 4-7: the loads by cp.async (bf16: straight into one of
-// three buffers; e4m3: codes, which their thread converts into one of two buffers).  Warp 8: the MMAs.  S of tile t + 1 is
-// issued when P V of tile t is done; a tile's chain S -> softmax -> P V takes
-// about 700 cycles, and two CTAs share an SM (one at head_dim 256).
+// Warps 0-3: softmax.  Warps 4-7: V, converted to f16 (e4m3); keys outside the part
+// cleared, and values that are not finite taken out of tiles where only some rows see
+// the key.  Warp 8: the MMAs; S of tile t + 1 goes to the second slot while the softmax
+// works on tile t.  Warp 9: the loads by TMA, one box per page and panel, three or four
+// stages ahead.  (Four warps issuing cp.async took 1000 to 2000 cycles a tile.)
+//
+// What bounds it: a tile's chain.  Softmax of a tile about 1200 cycles for 32 keys a
+// thread (its scheduler runs one softmax and one conversion warp), then 250 for the
+// signal to the MMA warp, 150 + 540 for P V, 250 + 450 for S of the tile after the next,
+// which needs the slot: about 1500 cycles a tile, whatever its size.  One CTA alone, 32
+// rows, e4m3: 7.6, 9.2 and 17 ns a key of head_dim 64, 128, 256; bf16 6.0, 7.7, 14.2,
+// where 512 CTAs run at 4.4, 5.8 and 6.2 TB/s.  More CTAs an SM (smaller tiles, one slot
+// of S) gave 41 ns a key of 512 CTAs of e4m3 and head_dim 128, one CTA with these 38.
 //
 // The weights, m and l are as in paged_attn.cuh.  Every wait is bounded.
 #pragma once
@@ -54,39 +62,39 @@ struct PagedTcParams {
 
 template <int D, bool FP8, int KG>
 struct PagedTcCfg {
-  static constexpr int BK = 64;
+  static constexpr int ESZ = FP8 ? 1 : 2;
+  static constexpr int BK = D == 256 ? 64 : 128;  // keys per tile
   static constexpr int RT = 128 / KG;        // query rows per CTA
-  static constexpr int NC = BK / KG;         // keys per softmax thread and tile
-  static constexpr int THREADS = 288;
-  static constexpr int PANEL = BK * 128;     // 64 keys x 64 columns of 2 bytes
-  static constexpr int TILE = PANEL * (D / 64);  // V of a tile, or K in bf16
-  // bf16: three buffers of K and V.  e4m3: two of V in f16, RAW tiles of V's codes on
-  // their way, and K's codes in a ring that holds those and the two in use
-  static constexpr int NBUF = FP8 ? 2 : 3;
-  static constexpr int RAW = FP8 ? (D == 64 ? 4 : 2) : 0;
-  static constexpr int RAW_TILE = FP8 ? BK * D + 32 : 0;  // codes of V, scales
-  static constexpr int NK = FP8 ? RAW + 2 : NBUF;
-  static constexpr int K_TILE = FP8 ? PANEL * (D > 128 ? 2 : 1) : TILE;  // 128 codes a row
-  static constexpr int V_OFF = NK * K_TILE;
-  static constexpr int RAW_OFF = V_OFF + NBUF * TILE;
-  static constexpr int TILES_END = RAW_OFF + RAW * RAW_TILE;
-  static constexpr int Q_COL = 64, O_COL = 64 + D / 2;  // S at column 0
-  static constexpr int TMEM_COLS = D == 256 ? 512 : 256;
-  static constexpr int CTAS = D == 256 || KG == 1 ? 1 : 2;  // (64 keys a thread need registers)
-  // bits of a tile's values that are not finite, [NBUF][2 signs][64 keys][D / 32], and
+  static constexpr int NC = BK / KG;         // keys per softmax thread and tile: 16 .. 128
+  static constexpr int THREADS = 320;
+  // K: panels of KROW bytes a key.  V in bf16 likewise; in e4m3 as codes [key][D], and
+  // converted to f16 in two buffers of 64-column panels.
+  static constexpr int KROW = D * ESZ < 128 ? 64 : 128;
+  static constexpr int KPANEL = BK * KROW;
+  static constexpr int VPANEL = BK * 128;
+  static constexpr int HALF = BK * D * ESZ;  // K or V of a stage
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int STAGES = FP8 ? 4 : 3;
+  static constexpr int NBUF = FP8 ? 2 : STAGES;  // tiles of V ready for the MMAs
+  static constexpr int VBUF = FP8 ? BK * D * 2 : 0;
+  static constexpr int VBUF_OFF = STAGES * STAGE;
+  static constexpr int TILES_END = VBUF_OFF + (FP8 ? NBUF * VBUF : 0);
+  // tensor memory: two slots of S, Q, O; 352, 448 or 512 columns
+  static constexpr int Q_COL = 2 * BK, O_COL = 2 * BK + D / 2;
+  static constexpr int TMEM_COLS = 512;
+  // bits of a tile's values that are not finite, [NBUF][2 signs][keys][D / 32], and
   // of what each of the 128 lanes has seen
   static constexpr int WORDS = D / 32;
-  static constexpr int STAGE_ROW = 68;       // floats: a chunk of 64 columns of O at the end
-  static constexpr int STAGE = 128 * STAGE_ROW * 4;
-  static constexpr int BAR_OFF = TILES_END > STAGE ? TILES_END : STAGE;
-  static constexpr int SCALE_OFF = BAR_OFF + 128;              // [NBUF][4] float2
-  static constexpr int FLAG_OFF = SCALE_OFF + NBUF * 32;       // [NBUF] ints, abort, tmem
+  static constexpr int OUT_ROW = 68;         // floats: a chunk of 64 columns of O at the end
+  static constexpr int OUT = 128 * OUT_ROW * 4;
+  static constexpr int BAR_OFF = TILES_END > OUT ? TILES_END : OUT;
+  static constexpr int FLAG_OFF = BAR_OFF + 192;               // [NBUF] ints, abort, tmem
   static constexpr int ML_OFF = FLAG_OFF + 32;                 // [128] m, l
-  static constexpr int BAD_OFF = ML_OFF + 128 * 8;             // [NBUF][2][64][WORDS]
-  static constexpr int SEEN_OFF = BAD_OFF + NBUF * 2 * 64 * WORDS * 4;  // [2][128][WORDS]
+  static constexpr int BAD_OFF = ML_OFF + 128 * 8;             // [NBUF][2][BK][WORDS]
+  static constexpr int SEEN_OFF = BAD_OFF + NBUF * 2 * BK * WORDS * 4;  // [2][128][WORDS]
   static constexpr int USED = SEEN_OFF + 2 * 128 * WORDS * 4 + 1024;  // 1024-byte alignment
-  // no third CTA on an SM: it would wait for tensor memory
-  static constexpr int SMEM = USED > 80 * 1024 ? USED : 80 * 1024;
+  // one CTA an SM: a second one would wait for tensor memory
+  static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
   static constexpr float OFFSET = FP8 ? 6.f : 0.f;
   static constexpr float RAISE = 8.f + OFFSET;
   static constexpr uint32_t FORMAT = FP8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // f16: zeros
@@ -118,6 +126,33 @@ __device__ __forceinline__ void mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
+// columns, token, head, page of a pool
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+// K-major operand of 64-byte rows with the 64-byte swizzle: 8-row atoms of 512 bytes
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;  // descriptor version for SM100
+  d |= static_cast<uint64_t>(4u) << 61;  // 64-byte swizzle
+  return d;
+}
+
+// one arrival for a warp whose lanes have fenced what they wrote: 128 single arrivals
+// on a barrier took about 800 cycles
+__device__ __forceinline__ void tc_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 // 2-byte values of a 16-byte chunk that are not finite: bits of columns (as +inf, -inf, both for
 // NaN); they are replaced by zeros
 template <bool FP8>
@@ -137,10 +172,12 @@ __device__ __forceinline__ void tc_clean(uint32_t (&w)[4], uint32_t* plus, uint3
 }
 
 template <int D, bool FP8, int KG>
-__global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
-    attn_paged_tc_kernel(const PagedTcParams tp) {
+__global__ void __launch_bounds__(320, 1)
+    attn_paged_tc_kernel(const __grid_constant__ CUtensorMap k_map,
+                         const __grid_constant__ CUtensorMap v_map, const PagedTcParams tp) {
   using C = PagedTcCfg<D, FP8, KG>;
-  constexpr int BK = C::BK, RT = C::RT, NC = C::NC, WORDS = C::WORDS, NBUF = C::NBUF;
+  constexpr int BK = C::BK, RT = C::RT, NC = C::NC, WORDS = C::WORDS, NBUF = C::NBUF,
+                STAGES = C::STAGES;
   const PagedParams& p = tp.a;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -149,16 +186,18 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   PagedPlace w{};
-  if (!w.find<D, RT, C::THREADS>(p)) return;
+  // parts begin at whole pages, so that a tile is whole boxes of the tensor maps
+  if (!w.find<D, RT, C::THREADS, 128>(p)) return;
   const int rows = w.rows, kb = w.kb, ke = w.ke;
   const int tiles = (ke - kb + BK - 1) / BK;
 
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // [NBUF] it is written
-  uint64_t* empty = full + NBUF;                                    // [NBUF] its P V is done
-  uint64_t* s_full = full + 2 * NBUF;
-  uint64_t* p_full = full + 2 * NBUF + 1;
-  float2* scales = reinterpret_cast<float2*>(smem + C::SCALE_OFF);
-  int* tile_bad = reinterpret_cast<int*>(smem + C::FLAG_OFF);       // [NBUF]
+  uint64_t* landed = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // [STAGES] TMA is done
+  uint64_t* left = landed + STAGES;  // [STAGES] the stage is free (bf16: P V is done)
+  uint64_t* ready = left + STAGES;   // [NBUF] V is ready for the MMAs (bf16: K and V)
+  uint64_t* used = ready + NBUF;     // [NBUF] e4m3: P V is done
+  uint64_t* s_full = used + NBUF;    // [2] a slot holds S,
+  uint64_t* p_full = s_full + 2;     // [2] or P
+  int* tile_bad = reinterpret_cast<int*>(smem + C::FLAG_OFF);         // [NBUF]
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF + 16);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::FLAG_OFF + 20);
   float2* ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
@@ -170,13 +209,19 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
     tmem_relinquish();
   }
   if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&landed[i], 1);
+      mbar_init(&left[i], FP8 ? 5 : 1);  // e4m3: S is done, four warps have converted V
+    }
     for (int i = 0; i < NBUF; ++i) {
-      mbar_init(&full[i], 128);
-      mbar_init(&empty[i], 1);
+      mbar_init(&ready[i], 4);
+      mbar_init(&used[i], 1);
       tile_bad[i] = 0;
     }
-    mbar_init(s_full, 1);
-    mbar_init(p_full, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+    }
     *abort = 0;
     fence_mbar_init();
   }
@@ -185,6 +230,12 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
   const uint32_t tmem = *tmem_at;
   auto mixed = [&](int t) {  // some key of the tile is seen by some rows only
     return kb + t * BK < w.in_lo || min(kb + t * BK + BK, ke) > w.in_hi;
+  };
+  // P V of tile t is done
+  auto wait_pv = [&](int t, uint32_t code) {
+    return FP8 ? mbar_wait(&used[t % NBUF], (t / NBUF) & 1, abort, tp.err, code, tp.timeout_ns)
+               : mbar_wait(&left[t % STAGES], (t / STAGES) & 1, abort, tp.err, code,
+                           tp.timeout_ns);
   };
 
   if (warp < 4) {
@@ -262,51 +313,92 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
     float m = -INFINITY, l = 0.f;
     bool poisoned = false;
     bool ok = true;
+    // scales of this warp's blocks of 16 keys: lane 2 i (K), 2 i + 1 (V) has block i's,
+    // of the next tile, and its page of the tile after that
+    constexpr int BLOCKS = NC / 16;
+    const int32_t* table = p.table + w.b * p.table_stride;
+    const float* my_scale = ((lane & 1) ? p.vc.scale : p.kc.scale) + w.h;
+    auto block_key = [&](int t) { return kb + t * BK + kg * NC + min(lane >> 1, BLOCKS - 1) * 16; };
+    auto block_page = [&](int t) {
+      return __ldg(table + (min(block_key(t), ke - 1) >> p.page_shift));
+    };
+    auto block_scale = [&](int t, uint32_t pg) {
+      return block_key(t) < ke && pg < static_cast<uint32_t>(p.num_pages)
+                 ? __ldg(my_scale + static_cast<int64_t>(pg) * p.hkv)
+                 : 0.f;
+    };
+    float next_scale = 0.f;
+    int next_page = 0;
+    if constexpr (FP8) {
+      next_scale = block_scale(0, block_page(0));
+      next_page = block_page(1);
+    }
     for (int t = 0; t < tiles; ++t) {
       const int b = t % NBUF;
-      if (!mbar_wait(&full[b], (t / NBUF) & 1, abort, tp.err, ERR_PAGED_SOFTMAX | 1,
-                     tp.timeout_ns) ||
-          !mbar_wait(s_full, t & 1, abort, tp.err, ERR_PAGED_SOFTMAX | 2, tp.timeout_ns))
+      // even lanes: K's factor; odd lanes: log2 and inverse of V's scale.  (Pages outside
+      // the pool have zeros: their keys count as x = 0 and V = 0.)
+      const float scale = next_scale == 0.f ? 1.f : next_scale;
+      const float log_or_k = (lane & 1) ? pg_lg2(scale) : scale, inverse = pg_rcp(scale);
+      if constexpr (FP8) {
+        next_scale = block_scale(t + 1, next_page);
+        next_page = block_page(t + 2);
+      }
+      auto factor = [&](int g) {  // never 0: a masked score stays -inf
+        return FP8 ? fmaxf(f_row * __shfl_sync(0xffffffffu, log_or_k, 2 * g), 1.2e-38f) : f_row;
+      };
+      auto log_scale = [&](int g) {
+        return FP8 ? __shfl_sync(0xffffffffu, log_or_k, 2 * g + 1) : 0.f;
+      };
+      auto inverse_scale_of = [&](int g) {
+        return FP8 ? __shfl_sync(0xffffffffu, inverse, 2 * g + 1) : 1.f;
+      };
+      if (!mbar_wait(&s_full[t & 1], (t >> 1) & 1, abort, tp.err, ERR_PAGED_SOFTMAX | 1,
+                     tp.timeout_ns))
         ok = false;
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      const uint32_t slot = lanes + (t & 1) * BK;
       uint32_t sr[NC];
       if constexpr (NC == 16)
-        tmem_ld16(lanes + kg * NC, sr);
+        tmem_ld16(slot + kg * NC, sr);
       else if constexpr (NC == 32)
-        tmem_ld32(lanes + kg * NC, sr);
+        tmem_ld32(slot + kg * NC, sr);
+      else if constexpr (NC == 64)
+        tmem_ld64(slot + kg * NC, sr);
       else
-        tmem_ld64(lanes, sr);
+        tmem_ld128(slot, sr);
       const int key0 = kb + t * BK + kg * NC;
       const bool edge = mixed(t) || kb + t * BK + BK > ke;
+      // (the common case runs without a branch between the blocks, so that their
+      // instructions overlap: a warp has its scheduler almost to itself)
+      if (capped || edge) {
+#pragma unroll
+        for (int g = 0; g < NC / 16; ++g) {
+          const float f = factor(g);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float x = __uint_as_float(sr[16 * g + i]);
+            if (capped) x = pg_cap(x * f * p.cap_mul, p.cap_log2);
+            const int key = key0 + 16 * g + i;
+            if (key < lo || key > hi) x = -INFINITY;
+            sr[16 * g + i] = __float_as_uint(x);
+          }
+        }
+      }
       float top = -INFINITY;
 #pragma unroll
       for (int g = 0; g < NC / 16; ++g) {
-        PagedScales sc;
-        if constexpr (FP8) sc = PagedScales(scales[b * 4 + kg * (NC / 16) + g]);
-        float f = fmaxf(f_row * sc.ks, 1.2e-38f);
-        if (capped) {
+        float v[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            sr[16 * g + i] = __float_as_uint(
-                pg_cap(__uint_as_float(sr[16 * g + i]) * f * p.cap_mul, p.cap_log2));
-          f = 1.f;
-        }
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int key = key0 + 16 * g + i;
-            if (key < lo || key > hi) sr[16 * g + i] = 0xff800000u;  // -inf
-          }
-        }
-        float v = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 16; i += 2)
-          v = fmax3(v, __uint_as_float(sr[16 * g + i]), __uint_as_float(sr[16 * g + i + 1]));
-        top = fmaxf(top, __fmaf_rn(v, f, sc.lv));
+        for (int i = 0; i < 4; ++i)
+          v[i] = fmaxf(fmax3(__uint_as_float(sr[16 * g + i]), __uint_as_float(sr[16 * g + 4 + i]),
+                             __uint_as_float(sr[16 * g + 8 + i])),
+                       __uint_as_float(sr[16 * g + 12 + i]));
+        top = fmaxf(top, __fmaf_rn(fmaxf(fmax3(v[0], v[1], v[2]), v[3]),
+                                   capped ? 1.f : factor(g), log_scale(g)));
       }
       const bool raise = top > m + C::RAISE;
       if (__any_sync(0xffffffffu, raise)) {
@@ -317,7 +409,14 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
           l *= a;
           m = to;
         }
-        if (t > 0) {  // P V of the tile before is done, or S would not be there
+        // O may be changed when P V of the tile before is done
+        if (t > 0 && !wait_pv(t - 1, ERR_PAGED_SOFTMAX | 2)) ok = false;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (t > 0) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -332,39 +431,60 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
       uint32_t pw[NC / 2];
 #pragma unroll
       for (int g = 0; g < NC / 16; ++g) {
-        PagedScales sc;
-        if constexpr (FP8) sc = PagedScales(scales[b * 4 + kg * (NC / 16) + g]);
-        const float f = capped ? 1.f : fmaxf(f_row * sc.ks, 1.2e-38f);
-        const float c = sc.lv - base;
-        float sum = 0.f;
+        const float f = capped ? 1.f : factor(g), c = log_scale(g) - base;
+        const uint64_t f2 = f2_pack(f, f), c2 = f2_pack(c, c);
+        uint64_t sum = f2_pack(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float x = pg_ex2(__fmaf_rn(__uint_as_float(sr[16 * g + 2 * i]), f, c));
-          const float y = pg_ex2(__fmaf_rn(__uint_as_float(sr[16 * g + 2 * i + 1]), f, c));
-          sum += x + y;
+          float x, y;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[16 * g + 2 * i]),
+                                   __uint_as_float(sr[16 * g + 2 * i + 1])),
+                           f2, c2),
+                    x, y);
+          x = pg_ex2(x);
+          y = pg_ex2(y);
+          sum = f2_add(sum, f2_pack(x, y));
           pw[8 * g + i] = FP8 ? pg_f16_pair(x, y) : bf16_pair(x, y);
         }
-        l = __fmaf_rn(sum, sc.iv, l);
+        float x, y;
+        f2_unpack(sum, x, y);
+        l = __fmaf_rn(x + y, inverse_scale_of(g), l);
       }
       // weights of this thread's keys, zeros for the other groups'
 #pragma unroll
       for (int g = 0; g < KG; ++g) {
         if constexpr (NC == 16) {
-          uint32_t x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = g == kg ? pw[i] : 0u;
-          tmem_st8(lanes + g * 8, x);
+          uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+          if (g == kg)
+            tmem_st8(slot + g * 8, pw);
+          else
+            tmem_st8(slot + g * 8, x);
         } else if constexpr (NC == 32) {
-          uint32_t x[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = g == kg ? pw[i] : 0u;
-          tmem_st16(lanes + g * 16, x);
+          uint32_t x[16] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+          if (g == kg)
+            tmem_st16(slot + g * 16, pw);
+          else
+            tmem_st16(slot + g * 16, x);
         } else {
-          tmem_st32(lanes, pw);
+#pragma unroll
+          for (int h = 0; h < NC / 64; ++h) {
+            uint32_t x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = g == kg ? pw[32 * h + i] : 0u;
+            tmem_st32(slot + g * (NC / 2) + h * 32, x);
+          }
         }
       }
       tmem_st_wait();
       tc_fence_before();
+      if (mixed(t)) {  // the values have been looked at
+        ok = mbar_wait(&ready[b], (t / NBUF) & 1, abort, tp.err, ERR_PAGED_SOFTMAX | 3,
+                       tp.timeout_ns);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+      }
       if (mixed(t) && tile_bad[b]) {
         // values that are not finite, taken out of the tile: noted for the rows that see them
         if (!poisoned) {
@@ -375,16 +495,15 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
           const int key = kb + t * BK + k;
           if (key < lo || key > hi) continue;
           for (int i = 0; i < WORDS; ++i) {
-            seen[tid * WORDS + i] |= bad[((b * 2 + 0) * 64 + k) * WORDS + i];
-            seen[(128 + tid) * WORDS + i] |= bad[((b * 2 + 1) * 64 + k) * WORDS + i];
+            seen[tid * WORDS + i] |= bad[((b * 2 + 0) * BK + k) * WORDS + i];
+            seen[(128 + tid) * WORDS + i] |= bad[((b * 2 + 1) * BK + k) * WORDS + i];
           }
         }
       }
-      mbar_arrive(p_full);
+      tc_arrive(&p_full[t & 1], lane);
     }
     const int last = tiles - 1;
-    if (ok) ok = mbar_wait(&empty[last % NBUF], (last / NBUF) & 1, abort, tp.err,
-                           ERR_PAGED_SOFTMAX | 3, tp.timeout_ns);
+    if (ok) ok = wait_pv(last, ERR_PAGED_SOFTMAX | 4);
     // O of the groups of a row, merged: in chunks of 64 columns through shared memory
     // (the buffers are free)
     ok = __all_sync(0xffffffffu, ok);
@@ -413,8 +532,8 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
         else if (p.lse)
           w.store_lse(p, r, l2);
       }
-      float* stage = reinterpret_cast<float*>(smem);  // [128][STAGE_ROW]
-      constexpr int SROW = C::STAGE_ROW;
+      float* stage = reinterpret_cast<float*>(smem);  // [128][OUT_ROW]
+      constexpr int SROW = C::OUT_ROW;
 #pragma unroll 1
       for (int c = 0; c < D; c += 64) {
 #pragma unroll
@@ -463,39 +582,16 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
     }
     tc_fence_before();
   } else if (warp < 8) {
-    // ------------------------------------------------------------------ loads
+    // ---------------------------------------------------- V for the MMAs (bf16: checked)
     const int lt = tid - 128;
-    constexpr int ESZ = FP8 ? 1 : 2;
-    constexpr int CPR = D * ESZ / 16;          // 16-byte pieces of a cached row
-    constexpr int STEP = 128 / CPR;            // rows between a thread's pieces
-    constexpr int N = BK / STEP;               // pieces of K (and of V) per thread and tile
+    constexpr int CPR = D * C::ESZ / 16;       // 16-byte pieces of a key's row
+    constexpr int STEP = 128 / CPR;            // keys between a thread's pieces
+    constexpr int N = BK / STEP;               // pieces of a thread and tile
     const int piece = lt % CPR, row0 = lt / CPR;
-    const uint8_t* kbase = p.kc.p + p.kc.s_head * ESZ * w.h + piece * 16;
-    const uint8_t* vbase = p.vc.p + p.vc.s_head * ESZ * w.h + piece * 16;
-    const int32_t* table = p.table + w.b * p.table_stride;
-    const int slot_mask = (1 << p.page_shift) - 1, last_entry = (ke - 1) >> p.page_shift;
-    const uint32_t spread = ke - w.klo;
-    int page[N];
-    auto find_pages = [&](int t) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        page[i] = __ldg(table + min((kb + t * BK + row0 + i * STEP) >> p.page_shift, last_entry));
-    };
-    // a piece's place in the pools; false: zeros
-    auto source = [&](int t, int i, uint64_t* ko, uint64_t* vo) {
-      const int key = kb + t * BK + row0 + i * STEP;
-      const uint32_t pg = page[i];
-      const bool live = static_cast<uint32_t>(key - w.klo) < spread &&
-                        pg < static_cast<uint32_t>(p.num_pages);
-      const uint32_t slot = key & slot_mask;
-      *ko = static_cast<uint64_t>(live ? pg : 0u) * p.k_page + static_cast<uint64_t>(slot) * p.k_token;
-      *vo = static_cast<uint64_t>(live ? pg : 0u) * p.v_page + static_cast<uint64_t>(slot) * p.v_token;
-      return live;
-    };
     // a tile with keys that only some rows see: values that are not finite are noted
     // and replaced by zeros, because a zero weight would not hide them
     auto clear_bad = [&](int b) {
-      for (int i = lt; i < 2 * 64 * WORDS; i += 128) bad[b * 2 * 64 * WORDS + i] = 0;
+      for (int i = lt; i < 2 * BK * WORDS; i += 128) bad[b * 2 * BK * WORDS + i] = 0;
       if (lt == 0) tile_bad[b] = 0;
       named_bar_sync(3, 128);
     };
@@ -503,63 +599,35 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
       uint32_t plus, minus;
       tc_clean<FP8>(x, &plus, &minus);
       if (plus | minus) {
-        atomicOr(&bad[((b * 2 + 0) * 64 + key) * WORDS + d0 / 32], plus << (d0 & 31));
-        atomicOr(&bad[((b * 2 + 1) * 64 + key) * WORDS + d0 / 32], minus << (d0 & 31));
+        atomicOr(&bad[((b * 2 + 0) * BK + key) * WORDS + d0 / 32], plus << (d0 & 31));
+        atomicOr(&bad[((b * 2 + 1) * BK + key) * WORDS + d0 / 32], minus << (d0 & 31));
         tile_bad[b] = 1;
       }
-      return (plus | minus) != 0;
     };
-    auto wait_empty = [&](int t) {
-      bool ok = t < NBUF || mbar_wait(&empty[t % NBUF], ((t / NBUF) + 1) & 1, abort, tp.err,
-                                   ERR_PAGED_LOAD | 1, tp.timeout_ns);
-      return __all_sync(0xffffffffu, ok) != 0;
-    };
-    if constexpr (FP8) {
-      // A thread converts the codes that it loaded itself, so it waits for its own
-      // copies only; they lie [piece][thread], every access in different banks.
-      const uint32_t mine = sbase + C::RAW_OFF + lt * 16;
-      auto issue = [&](int t) {
-        const uint32_t st = mine + (t % C::RAW) * C::RAW_TILE;
-        const uint32_t kd = sbase + (t % C::NK) * C::K_TILE + (piece >> 3) * C::PANEL;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          uint64_t ko, vo;
-          const bool live = source(t, i, &ko, &vo);
-          pg_cp16(kd + tc_chunk(row0 + i * STEP, piece & 7), kbase + ko, live);
-          pg_cp16(st + i * 2048, vbase + vo, live);
-        }
-        if (lt < 8) {  // scales of the tile's four 16-key blocks
-          const int key = kb + t * BK + (lt >> 1) * 16;
-          const uint32_t pg = __ldg(table + min(key >> p.page_shift, last_entry));
-          const bool live = key < ke && pg < static_cast<uint32_t>(p.num_pages);
-          pg_cp4(sbase + C::RAW_OFF + (t % C::RAW) * C::RAW_TILE + BK * D + lt * 4,
-                 ((lt & 1) ? p.vc.scale : p.kc.scale) +
-                     static_cast<int64_t>(live ? pg : 0u) * p.hkv + w.h,
-                 live);
-        }
-      };
-      find_pages(0);
-#pragma unroll 1
-      for (int t = 0; t < C::RAW; ++t) {
-        if (t < tiles) issue(t);
-        pg_commit();
-        find_pages(t + 1);  // (past the last tile: the last entry again)
-      }
-      for (int t = 0; t < tiles; ++t) {
-        const int b = t % NBUF;
-        pg_wait<C::RAW - 1>();
-        if (!wait_empty(t)) break;
-        const bool mix = mixed(t);
-        if (mix) clear_bad(b);
-        const uint8_t* codes = smem + C::RAW_OFF + (t % C::RAW) * C::RAW_TILE;
-        const uint32_t vd = sbase + C::V_OFF + b * C::TILE + (piece >> 2) * C::PANEL;
+    for (int t = 0; t < tiles; ++t) {
+      const int b = t % NBUF, st = t % STAGES, key0 = kb + t * BK;
+      bool ok = mbar_wait(&landed[st], (t / STAGES) & 1, abort, tp.err, ERR_PAGED_LOAD | 1,
+                          tp.timeout_ns);
+      if (FP8 && ok && t >= NBUF) ok = wait_pv(t - NBUF, ERR_PAGED_LOAD | 2);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const bool mix = mixed(t);
+      const bool edge = key0 < w.klo || key0 + BK > ke;  // rows that are not this part's: zeros
+      if (mix) clear_bad(b);
+      uint8_t* codes = smem + st * C::STAGE + C::HALF;
+      if constexpr (FP8) {
+        const uint32_t vd = sbase + C::VBUF_OFF + b * C::VBUF + (piece >> 2) * C::VPANEL;
         // the two chunks of a piece; the lanes of an odd panel take them in the other
         // order, so that the 8 lanes of a store lie in different banks
         const int swap = (piece >> 2) & 1, c0 = 2 * (piece & 3) + swap;
+        uint4 v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          v[i] = *reinterpret_cast<const uint4*>(codes + (row0 + i * STEP) * D + piece * 16);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int key = row0 + i * STEP;
-          const uint4 x = *reinterpret_cast<const uint4*>(codes + i * 2048 + lt * 16);
+          uint4 x = v[i];
+          if (edge && (key0 + key < w.klo || key0 + key >= ke)) x = make_uint4(0, 0, 0, 0);
           const uint32_t w0 = swap ? x.z : x.x, w1 = swap ? x.w : x.y;
           const uint32_t w2 = swap ? x.x : x.z, w3 = swap ? x.y : x.w;
           uint32_t first[4] = {pg_f16_lo(w0), pg_f16_hi(w0), pg_f16_lo(w1), pg_f16_hi(w1)};
@@ -571,105 +639,124 @@ __global__ void __launch_bounds__(288, PagedTcCfg<D, FP8, KG>::CTAS)
           st_shared16(vd + tc_chunk(key, c0), first[0], first[1], first[2], first[3]);
           st_shared16(vd + tc_chunk(key, c0 ^ 1), second[0], second[1], second[2], second[3]);
         }
-        if (lt < 8)
-          reinterpret_cast<float*>(scales + b * 4)[lt] =
-              reinterpret_cast<const float*>(codes + BK * D)[lt];
         fence_async_smem();
-        mbar_arrive(&full[b]);
-        if (t + C::RAW < tiles) issue(t + C::RAW);
-        pg_commit();
-        find_pages(t + C::RAW + 1);
-      }
-      pg_wait<0>();
-    } else {
-      // two tiles are on their way while one is handed over and used
-      auto issue = [&](int t) {
-        const int b = t % NBUF;
-        const uint32_t kd = sbase + b * C::TILE + (piece >> 3) * C::PANEL;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          uint64_t ko, vo;
-          const bool live = source(t, i, &ko, &vo);
-          const uint32_t o = tc_chunk(row0 + i * STEP, piece & 7);
-          pg_cp16(kd + o, kbase + ko, live);
-          pg_cp16(kd + C::V_OFF + o, vbase + vo, live);
-        }
-      };
-      find_pages(0);
-#pragma unroll 1
-      for (int t = 0; t < NBUF - 1; ++t) {
-        if (t < tiles) issue(t);
-        pg_commit();
-        find_pages(t + 1);
-      }
-      for (int t = 0; t < tiles; ++t) {
-        const int b = t % NBUF;
-        pg_wait<NBUF - 2>();
-        if (mixed(t)) {
-          clear_bad(b);
-          const uint32_t vd = sbase + C::V_OFF + b * C::TILE + (piece >> 3) * C::PANEL;
+        tc_arrive(&ready[b], lane);
+        if (lane == 0) mbar_arrive(&left[st]);
+      } else {
+        if (mix || edge) {
           for (int i = 0; i < N; ++i) {
             const int key = row0 + i * STEP;
-            uint4* at = reinterpret_cast<uint4*>(smem + (vd - sbase) + tc_chunk(key, piece & 7));
+            uint4* at = reinterpret_cast<uint4*>(codes + (piece >> 3) * C::VPANEL +
+                                                 tc_chunk(key, piece & 7));
             const uint4 x = *at;
             uint32_t y[4] = {x.x, x.y, x.z, x.w};
-            if (clean(b, key, piece * 8, y)) *at = make_uint4(y[0], y[1], y[2], y[3]);
+            if (key0 + key < w.klo || key0 + key >= ke)
+              y[0] = y[1] = y[2] = y[3] = 0;
+            else if (mix)
+              clean(b, key, piece * 8, y);
+            *at = make_uint4(y[0], y[1], y[2], y[3]);
           }
+          fence_async_smem();
         }
-        fence_async_smem();
-        mbar_arrive(&full[b]);
-        if (t + NBUF - 1 < tiles) {
-          if (!wait_empty(t + NBUF - 1)) break;
-          issue(t + NBUF - 1);
-        }
-        pg_commit();
-        find_pages(t + NBUF);
+        tc_arrive(&ready[b], lane);
       }
-      pg_wait<0>();
     }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ loads
+    const int tokens = min(1 << p.page_shift, BK), boxes = BK / tokens;  // of a tile: 1 .. 8
+    const int32_t* table = p.table + w.b * p.table_stride;
+    auto box_key = [&](int t) { return kb + t * BK + min(lane, boxes - 1) * tokens; };
+    auto box_page = [&](int t) { return __ldg(table + (min(box_key(t), ke - 1) >> p.page_shift)); };
+    int next_page = box_page(0);
+    int t = 0;
+    for (; t < tiles; ++t) {
+      const int st = t % STAGES, page = next_page, key = box_key(t);
+      next_page = box_page(t + 1);
+      if (t >= STAGES && !mbar_wait_warp(&left[st], ((t / STAGES) + 1) & 1, abort, tp.err,
+                                         ERR_PAGED_LOAD | 3, tp.timeout_ns))
+        break;
+      const bool live = lane < boxes && key < ke;
+      const int n = __popc(__ballot_sync(0xffffffffu, live));
+      if (lane == 0) mbar_expect_tx(&landed[st], n * tokens * D * C::ESZ * 2);
+      __syncwarp();
+      if (live) {
+        const int slot = key & ((1 << p.page_shift) - 1);
+        const uint32_t kd = sbase + st * C::STAGE + lane * tokens * C::KROW;
+#pragma unroll
+        for (int c = 0; c < C::HALF / C::KPANEL; ++c)
+          tma_load_4d(kd + c * C::KPANEL, &k_map, &landed[st], c * (C::KROW / C::ESZ), slot, w.h,
+                      page);
+        if constexpr (FP8) {
+          tma_load_4d(sbase + st * C::STAGE + C::HALF + lane * tokens * D, &v_map, &landed[st], 0,
+                      slot, w.h, page);
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(kd + C::HALF + c * C::VPANEL, &v_map, &landed[st], c * 64, slot, w.h, page);
+        }
+      }
+      __syncwarp();
+    }
+    if (t < tiles)  // gave up: the copies under way land before the memory goes
+      for (int u = max(0, t - STAGES); u < t; ++u)
+        mbar_wait_drain(&landed[u % STAGES], (u / STAGES) & 1, tp.timeout_ns);
   } else {
     // ------------------------------------------------------------------- MMAs
     named_bar_sync(1, 160);
     tc_fence_after();
-    const uint64_t kdesc = sdesc_sw128(sbase, 16, 1024);
-    const uint64_t vdesc = sdesc_sw128(sbase + C::V_OFF, C::PANEL, 1024);
-    for (int t = 0; t < tiles; ++t) {
-      const int b = t % NBUF;
-      const uint64_t kt = kdesc + static_cast<uint64_t>(t % C::NK) * (C::K_TILE >> 4);
-      const uint64_t vt = vdesc + static_cast<uint64_t>(b) * (C::TILE >> 4);
-      // the tile is there; S is free: P V of the tile before has read P
-      if (!mbar_wait_warp(&full[b], (t / NBUF) & 1, abort, tp.err, ERR_PAGED_MMA | 1,
-                          tp.timeout_ns))
-        break;
-      if (t > 0 && !mbar_wait_warp(&empty[(t - 1) % NBUF], ((t - 1) / NBUF) & 1, abort, tp.err,
-                                   ERR_PAGED_MMA | 2, tp.timeout_ns))
-        break;
+    const uint64_t kdesc = C::KROW == 64 ? sdesc_sw64(sbase, 512) : sdesc_sw128(sbase, 16, 1024);
+    const uint64_t vdesc =
+        sdesc_sw128(sbase + (FP8 ? C::VBUF_OFF : C::HALF), C::VPANEL, 1024);
+    auto issue_s = [&](int t) {
+      const int st = t % STAGES;
+      const uint64_t kt = kdesc + static_cast<uint64_t>(st) * (C::STAGE >> 4);
+      const uint32_t d = tmem + (t & 1) * BK;
+      if (!mbar_wait_warp(FP8 ? &landed[st] : &ready[st], (t / STAGES) & 1, abort, tp.err,
+                          ERR_PAGED_MMA | 1, tp.timeout_ns))
+        return false;
       tc_fence_after();
       if constexpr (FP8) {
+        constexpr int KS = D / 32;  // steps of 32 columns, for both parts of Q
 #pragma unroll
-        for (int k = 0; k < 2 * (D / 32); ++k) {  // both parts of Q, 32 columns of the head each
-          const int c = k % (D / 32);
-          mma_ts_f8(tmem, tmem + C::Q_COL + k * 8, kt + (c >> 2) * (C::PANEL >> 4) + (c & 3) * 2,
+        for (int k = 0; k < 2 * KS; ++k) {
+          const int c = k % KS;
+          mma_ts_f8(d, tmem + C::Q_COL + k * 8, kt + (c >> 2) * (C::KPANEL >> 4) + (c & 3) * 2,
                     C::IDESC_S, k != 0);
         }
       } else {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ts(tmem, tmem + C::Q_COL + k * 8, kt + (k >> 2) * (C::PANEL >> 4) + (k & 3) * 2,
+          mma_ts(d, tmem + C::Q_COL + k * 8, kt + (k >> 2) * (C::KPANEL >> 4) + (k & 3) * 2,
                  C::IDESC_S, k != 0);
       }
-      mma_commit(s_full);
-      if (!mbar_wait_warp(p_full, t & 1, abort, tp.err, ERR_PAGED_MMA | 3, tp.timeout_ns)) break;
+      mma_commit(&s_full[t & 1]);
+      if (FP8) mma_commit(&left[st]);
+      return true;
+    };
+    bool ok = issue_s(0);
+    for (int t = 0; ok && t < tiles; ++t) {
+      const int b = t % NBUF;
+      // S of the next tile while the softmax works on this one; its slot is free when
+      // P V of the tile before has read P
+      if (t + 1 < tiles) {
+        ok = t == 0 || __all_sync(0xffffffffu, wait_pv(t - 1, ERR_PAGED_MMA | 2));
+        if (!ok || !issue_s(t + 1)) break;
+      }
+      if (!mbar_wait_warp(&p_full[t & 1], (t >> 1) & 1, abort, tp.err, ERR_PAGED_MMA | 3,
+                          tp.timeout_ns) ||
+          (FP8 && !mbar_wait_warp(&ready[b], (t / NBUF) & 1, abort, tp.err, ERR_PAGED_MMA | 4,
+                                  tp.timeout_ns)))
+        break;
       tc_fence_after();
+      const uint64_t vt = vdesc + static_cast<uint64_t>(b) * ((FP8 ? C::VBUF : C::STAGE) >> 4);
 #pragma unroll
       for (int k = 0; k < BK / 16; ++k)
-        mma_ts(tmem + C::O_COL, tmem + k * 8, vt + k * (16 * 128 >> 4), C::IDESC_O,
+        mma_ts(tmem + C::O_COL, tmem + (t & 1) * BK + k * 8, vt + k * (16 * 128 >> 4), C::IDESC_O,
                (t | k) != 0);
-      mma_commit(&empty[b]);
+      mma_commit(FP8 ? &used[b] : &left[b]);
     }
     // a CTA that gave up: what was issued has to end before its memory goes
     if (*abort) {
-      mma_commit(s_full);
       const uint64_t t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 100000) {  // 100 us, far above any tile's MMAs
       }

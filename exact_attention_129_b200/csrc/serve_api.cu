@@ -1,5 +1,6 @@
 // serve_api.cu -- the C ABI of rotary positions and of the paged key/value
 // cache: argument checks, kernel choice and launches.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -18,6 +19,7 @@ namespace attn {
 // api.cu
 uint32_t* device_error_word();
 uint64_t device_wait_timeout_ns();
+void* tensor_map_encoder();
 
 namespace {
 
@@ -208,10 +210,17 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 constexpr double kHbmBytesPerNs = 6500.0;   // measured copy rate
 constexpr int64_t kDenseBytes = int64_t(4) << 30;  // the packed copies may take so much
 
-// ns per key of one CTA of the paged kernel, by head_dim 64, 128, 256 and 8, 16,
-// 32, 64 rows: the same, up to a tenth, with one or two CTAs on an SM
-constexpr double kPagedNsPerKey[3][4] = {{8.4, 9.6, 15., 26.}, {12., 15., 22., 37.},
-                                         {21., 27., 36., 63.}};
+// Query rows per CTA: 8, and in e4m3 16, of the mma.sync kernel; 32, 64 or 128 of the
+// tcgen05 kernel.  512 CTAs of 16 rows of head_dim 64, 128, 256: e4m3 24, 32, 61 ns a key
+// in the mma.sync kernel, 29, 36, 67 in the other; bf16 29, 46, 120 and 29, 44, 82.
+constexpr int kPagedRows[5] = {8, 16, 32, 64, 128};
+// ns per key of one CTA, by type, head_dim and rows, where HBM does not set the pace
+constexpr double kPagedNsPerKey[2][3][5] = {{{9., 0., 6., 7., 11.},
+                                             {15., 0., 7.7, 8.2, 12.},
+                                             {23., 0., 14.2, 15., 16.2}},
+                                            {{8.4, 10.2, 7.7, 9.6, 17.6},
+                                             {11., 14., 9.8, 12., 21.},
+                                             {20.5, 25., 18., 19.5, 23.}}};
 // ns per key of one CTA of attn_fwd (its query tile against one key)
 constexpr double kDenseNsPerKey[3] = {15., 17.7, 21.};
 
@@ -220,33 +229,39 @@ struct PagedShape {
   int d, d_index, key_bytes;  // key_bytes: of K and V of one key and head
 };
 
-constexpr double kRoundNs = 3000.0;  // a CTA's set-up and drain
+constexpr double kRoundNs[2] = {3000.0, 6000.0};  // a CTA's set-up and drain: mma.sync, tcgen05
 constexpr double kMergeCopies = 3.0;  // the parts of O cross HBM or L2 about so often
 
 // one round of k CTAs of chunk keys side by side
-double round_ns(int64_t k, double chunk, double ns_per_key, double key_bytes) {
-  return kRoundNs + std::max(chunk * ns_per_key, k * chunk * key_bytes / kHbmBytesPerNs);
+double round_ns(int64_t k, double chunk, double ns_per_key, double key_bytes, double fixed) {
+  return fixed + std::max(chunk * ns_per_key, k * chunk * key_bytes / kHbmBytesPerNs);
 }
 // n CTAs of equal length: whole rounds of `slots`, then the rest
-double rounds_ns(int64_t n, int64_t slots, double chunk, double ns_per_key, double key_bytes) {
+double rounds_ns(int64_t n, int64_t slots, double chunk, double ns_per_key, double key_bytes,
+                 double fixed) {
   const int64_t full = n / slots, rest = n % slots;
-  return full * round_ns(slots, chunk, ns_per_key, key_bytes) +
-         (rest ? round_ns(rest, chunk, ns_per_key, key_bytes) : 0.0);
+  return full * round_ns(slots, chunk, ns_per_key, key_bytes, fixed) +
+         (rest ? round_ns(rest, chunk, ns_per_key, key_bytes, fixed) : 0.0);
 }
 // n CTAs of differing lengths: a free slot takes the next one, half a CTA is left over
-double ragged_ns(double n, int64_t slots, double chunk, double ns_per_key, double key_bytes) {
-  if (n <= slots) return round_ns(static_cast<int64_t>(n), chunk, ns_per_key, key_bytes);
-  return n / slots * round_ns(slots, chunk, ns_per_key, key_bytes) +
-         0.5 * round_ns(0, chunk, ns_per_key, key_bytes);
+double ragged_ns(double n, int64_t slots, double chunk, double ns_per_key, double key_bytes,
+                 double fixed) {
+  if (n <= slots) return round_ns(static_cast<int64_t>(n), chunk, ns_per_key, key_bytes, fixed);
+  return n / slots * round_ns(slots, chunk, ns_per_key, key_bytes, fixed) +
+         0.5 * round_ns(0, chunk, ns_per_key, key_bytes, fixed);
 }
 
 double paged_plan_tiles(const PagedShape& x, int want, int sms, PagedPlan* pl) {
-  const int rt = x.rows <= 8 ? 8 : x.rows <= 32 ? 32 : x.rows <= 64 ? 64 : 128;
-  const int ri = rt == 8 ? 0 : rt == 32 ? 1 : rt == 64 ? 2 : 3;
+  const bool e4m3 = x.key_bytes == 2 * x.d;
+  const int ri =
+      x.rows <= 8 ? 0 : e4m3 && x.rows <= 16 ? 1 : x.rows <= 32 ? 2 : x.rows <= 64 ? 3 : 4;
+  const int rt = kPagedRows[ri];
   pl->rt = rt;
   pl->row_tiles = static_cast<int>((x.rows + rt - 1) / rt);
   const int64_t per_part = x.units * pl->row_tiles;
-  const int64_t slots = static_cast<int64_t>(sms) * (x.key_bytes > 512 ? 1 : rt == 8 ? 3 : 2);
+  // CTAs that share an SM
+  const int64_t slots = static_cast<int64_t>(sms) * (ri > 1 || x.key_bytes > 512 ? 1 : 3 - ri);
+  const double key = kPagedNsPerKey[e4m3][x.d_index][ri], fixed = kRoundNs[ri > 1];
   auto chunk_of = [&](int64_t splits) {  // whole tiles of every kernel
     return std::max<int64_t>(128, ((x.span + splits - 1) / splits + 127) / 128 * 128);
   };
@@ -254,12 +269,12 @@ double paged_plan_tiles(const PagedShape& x, int want, int sms, PagedPlan* pl) {
   int64_t splits = 0;
   for (int s = want ? want : 1; s <= (want ? want : kPagedMaxSplits); s += 1 + s / 8) {
     const int64_t chunk = chunk_of(s), parts = (x.span + chunk - 1) / chunk;
-    const double c = static_cast<double>(chunk), key = kPagedNsPerKey[x.d_index][ri];
+    const double c = static_cast<double>(chunk);
     // max_k bounds the lengths, which are not known here: as if half the batches
     // were of equal sequences and half of sequences of 0.6 of it on average
-    double t = 4000. + rounds_ns(per_part * parts, slots, c, key, x.key_bytes);
+    double t = 4000. + rounds_ns(per_part * parts, slots, c, key, x.key_bytes, fixed);
     if (x.batch > 1)
-      t = 0.5 * (t + 4000. + ragged_ns(0.6 * per_part * parts, slots, c, key, x.key_bytes));
+      t = 0.5 * (t + 4000. + ragged_ns(0.6 * per_part * parts, slots, c, key, x.key_bytes, fixed));
     if (parts > 1)
       t += 2000. + kMergeCopies * 8. * parts * x.total_q * x.hq * x.d / kHbmBytesPerNs;
     if (!splits || t < best) best = t, splits = parts;
@@ -277,17 +292,17 @@ double paged_plan_tiles(const PagedShape& x, int want, int sms, PagedPlan* pl) {
 bool paged_plan_dense(const PagedShape& x, int hkv, int sms, double limit, PagedPlan* pl) {
   const int64_t key_rows = x.batch * (x.max_k + kGatherPad);
   const int64_t copy = key_rows * hkv * x.d * 2;
-  if (x.rows < 64 || x.batch > 32767 || 2 * copy > kDenseBytes || key_rows >= (1 << 30))
+  if (x.rows < 128 || x.batch > 32767 || 2 * copy > kDenseBytes || key_rows >= (1 << 30))
     return false;
-  // code read, copy written and read; two launches more
-  const double gather = 8000. + key_rows * hkv * (x.key_bytes + 8. * x.d) / kHbmBytesPerNs;
+  // code read, copy written and read; three launches more
+  const double gather = 16000. + key_rows * hkv * (x.key_bytes + 8. * x.d) / kHbmBytesPerNs;
   const int64_t tile = x.d == 256 ? 128 : 256;
   const int64_t ctas = x.units * ((x.rows + tile - 1) / tile);
   double best = 0;
   int splits = 0;
   for (int s = 1; s <= 16 && x.max_k >= 512 * s; s *= 2) {
     double t = gather + rounds_ns(ctas * s, sms, static_cast<double>(x.span) / s,
-                                  kDenseNsPerKey[x.d_index], 0.0);
+                                  kDenseNsPerKey[x.d_index], 0.0, kRoundNs[0]);
     if (s > 1) t += 4000. + kMergeCopies * 8. * s * x.total_q * x.hq * x.d / kHbmBytesPerNs;
     if (!splits || t < best) best = t, splits = s;
   }
@@ -322,12 +337,12 @@ PagedPlan paged_plan(const attn_paged_cache_t* c, int batch, int total_q, int ma
   x.d_index = x.d == 64 ? 0 : x.d == 128 ? 1 : 2;
   x.key_bytes = 2 * x.d * (c->type == ATTN_CACHE_E4M3 ? 1 : 2);
   // keys a CTA's rows can see: with both bounds, the window and the rows' spread;
-  // parts begin at a multiple of 16
+  // parts begin at a multiple of 16 or 128
   x.span = max_k;
   if (lo_off < kPagedNoBound && hi_off < kPagedNoBound)
     x.span = std::min<int64_t>(x.span, static_cast<int64_t>(lo_off) + hi_off + 2 +
                                            (64 + x.group - 1) / x.group);
-  if (lo_off < kPagedNoBound) x.span += 15;
+  if (lo_off < kPagedNoBound) x.span += 127;
   x.span = std::max<int64_t>(x.span, 1);
   const double t = paged_plan_tiles(x, want, sms, &pl);
   PagedPlan dense{};
@@ -368,8 +383,8 @@ attn_status_t paged_sizes(const attn_paged_cache_t* c, int32_t batch, int32_t to
 
 // raises a kernel's shared memory limit once per device, launches it and, for
 // keys in parts, the merge
-template <int D, auto Kernel, int THREADS, int SMEM, class Params>
-attn_status_t launch_paged(const PagedParams& p, const Params& kp, int batch, cudaStream_t s) {
+template <int D, auto Kernel, int THREADS, int SMEM, class... Args>
+attn_status_t launch_paged(const PagedParams& p, int batch, cudaStream_t s, const Args&... args) {
   static bool ready[kServeDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
@@ -381,7 +396,7 @@ attn_status_t launch_paged(const PagedParams& p, const Params& kp, int batch, cu
   }
   const int64_t ctas = static_cast<int64_t>(batch) * p.num_splits * p.row_tiles * p.hkv;
   if (ctas > kMaxGrid) return ATTN_ERR_INVALID_ARG;
-  Kernel<<<static_cast<unsigned>(ctas), THREADS, SMEM, s>>>(kp);
+  Kernel<<<static_cast<unsigned>(ctas), THREADS, SMEM, s>>>(args...);
   attn_status_t st = launched();
   if (st != ATTN_OK || p.num_splits == 1) return st;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.hq;
@@ -400,12 +415,48 @@ attn_status_t launch_paged(const PagedParams& p, const Params& kp, int batch, cu
              : ATTN_ERR_CUDA;
 }
 
+// a pool as (columns, token, head, page) with boxes of box_cols x tokens of one page
+// and head
+bool pool_map(CUtensorMap* map, const CacheView& c, const PagedParams& p, int d, int esz,
+              int box_cols, int tokens, CUtensorMapSwizzle swizzle) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  const Encode encode = reinterpret_cast<Encode>(tensor_map_encoder());
+  if (!encode) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), cuuint64_t(1) << p.page_shift,
+                              static_cast<cuuint64_t>(p.hkv),
+                              static_cast<cuuint64_t>(std::max(p.num_pages, 1))};
+  // (the stride of a dimension of 1 is never used, and may be anything)
+  auto stride = [&](int64_t s, cuuint64_t n) {
+    return static_cast<cuuint64_t>(n > 1 ? s * esz : static_cast<int64_t>(d) * esz);
+  };
+  const cuuint64_t strides[3] = {stride(c.s_token, dims[1]), stride(c.s_head, dims[2]),
+                                 stride(c.s_page, dims[3])};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(tokens), 1,
+                             1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return encode(map, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                c.p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool FP8, int KG>
 attn_status_t launch_tc(const PagedParams& p, int batch, cudaStream_t s) {
   using C = PagedTcCfg<D, FP8, KG>;
   const PagedTcParams tp{p, device_error_word(), device_wait_timeout_ns()};
   if (!tp.err) return ATTN_ERR_CUDA;
-  return launch_paged<D, attn_paged_tc_kernel<D, FP8, KG>, C::THREADS, C::SMEM>(p, tp, batch, s);
+  const int tokens = std::min(1 << p.page_shift, C::BK);
+  CUtensorMap k, v;
+  if (!pool_map(&k, p.kc, p, D, C::ESZ, C::KROW / C::ESZ, tokens,
+                C::KROW == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !pool_map(&v, p.vc, p, D, C::ESZ, FP8 ? D : 64, tokens,
+                FP8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
+    return ATTN_ERR_CUDA;
+  return launch_paged<D, attn_paged_tc_kernel<D, FP8, KG>, C::THREADS, C::SMEM>(p, batch, s, k, v,
+                                                                               tp);
 }
 
 template <int D, bool FP8>
@@ -413,8 +464,12 @@ attn_status_t launch_paged_rows(const PagedParams& p, const PagedPlan& pl, int b
                                 cudaStream_t s) {
   switch (pl.rt) {
     case 8:
-      return launch_paged<D, attn_paged_kernel<D, FP8, 1, 1>, 128, PagedCfg<D, FP8, 1, 1>::SMEM>(
-          p, p, batch, s);
+      return launch_paged<D, attn_paged_kernel<D, FP8, 1>, 128, PagedCfg<D, FP8, 1>::SMEM>(
+          p, batch, s, p);
+    case 16:
+      if constexpr (FP8)
+        return launch_paged<D, attn_paged_kernel<D, FP8, 2>, 128, PagedCfg<D, FP8, 2>::SMEM>(
+            p, batch, s, p);
     case 32: return launch_tc<D, FP8, 4>(p, batch, s);
     case 64: return launch_tc<D, FP8, 2>(p, batch, s);
     default: return launch_tc<D, FP8, 1>(p, batch, s);
