@@ -103,7 +103,7 @@ attn_status_t check_cache(const attn_paged_cache_t* c) {
   for (int64_t s : {c->k_s_page, c->k_s_token, c->k_s_head, c->v_s_page, c->v_s_token,
                     c->v_s_head})
     if (s % step != 0 || s < 0 || s >= kMaxStride) return ATTN_ERR_INVALID_ARG;
-  if (c->num_pages < 0 || c->pages_per_seq < 0 || c->nheads_kv < 1 || c->nheads_kv > 65535)
+  if (c->num_pages < 1 || c->pages_per_seq < 0 || c->nheads_kv < 1 || c->nheads_kv > 65535)
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
@@ -427,7 +427,7 @@ bool pool_map(CUtensorMap* map, const CacheView& c, const PagedParams& p, int d,
   if (!encode) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), cuuint64_t(1) << p.page_shift,
                               static_cast<cuuint64_t>(p.hkv),
-                              static_cast<cuuint64_t>(std::max(p.num_pages, 1))};
+                              static_cast<cuuint64_t>(p.num_pages)};
   // (the stride of a dimension of 1 is never used, and may be anything)
   auto stride = [&](int64_t s, cuuint64_t n) {
     return static_cast<cuuint64_t>(n > 1 ? s * esz : static_cast<int64_t>(d) * esz);

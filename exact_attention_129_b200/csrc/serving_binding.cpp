@@ -15,9 +15,13 @@
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <sstream>
+#include <stdexcept>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "attn.h"
 
@@ -35,11 +39,15 @@ struct Abi {
 Abi abi;
 PyObject* attn_error = nullptr;
 
-// thrown by the checks -> ValueError; by a refused call -> AttnError(name, code)
-struct BadValue {
-  std::string text;
+// thrown by the checks -> ValueError; by a refused call -> AttnError(name, code).
+// (std::exceptions, because a backward runs in a thread of the autograd engine, which
+// carries those to the caller and ends the process for any other.)
+struct BadValue : std::runtime_error {
+  using std::runtime_error::runtime_error;
 };
-struct Refused {
+struct Refused : std::runtime_error {
+  Refused(const char* n, int c)
+      : std::runtime_error(std::string(n) + ": status " + std::to_string(c)), name(n), code(c) {}
   const char* name;
   int code;
 };
@@ -48,7 +56,7 @@ template <class... A>
 [[noreturn]] void bad(const A&... a) {
   std::ostringstream s;
   (s << ... << a);
-  throw BadValue{s.str()};
+  throw BadValue(s.str());
 }
 
 struct Rows {  // a [tokens, heads, head_dim] tensor as the C ABI takes it
@@ -76,17 +84,27 @@ Rows rows_of(const char* name, const Tensor& t, c10::Device dev) {
   return {t.data_ptr(), s[0], s[1]};
 }
 
+// strides under which no two elements share memory: each one past what those below it span
+bool disjoint(const Tensor& t) {
+  std::vector<std::pair<int64_t, int64_t>> dims;
+  for (int64_t i = 0; i < t.dim(); ++i)
+    if (t.size(i) > 1) dims.emplace_back(t.stride(i), t.size(i));
+  std::sort(dims.begin(), dims.end());
+  int64_t span = 1;
+  for (const auto& [stride, n] : dims) {
+    if (stride < span) return false;
+    span += stride * (n - 1);
+  }
+  return true;
+}
+
 // an output for the rows `src`: other memory, or the very same
 Rows out_rows(const char* name, const Tensor& t, const Tensor& src, c10::Device dev) {
   const Rows r = rows_of(name, t, dev);
   if (t.sizes() != src.sizes())
     bad(name, " must have shape ", src.sizes(), ", got ", t.sizes());
   // no two threads may write one element
-  int64_t a = std::abs(r.st), an = t.size(0), b = std::abs(r.sh), bn = t.size(1);
-  if (a > b) std::swap(a, b), std::swap(an, bn);
-  const int64_t d = t.size(2);
-  if ((an > 1 && a < d) || (bn > 1 && b < (an > 0 ? a * (an - 1) : 0) + d))
-    bad(name, " overlaps itself, strides ", t.strides());
+  if (!disjoint(t)) bad(name, " overlaps itself, strides ", t.strides());
   return r;
 }
 
@@ -179,7 +197,7 @@ void rotary_run(const Tensor& q, const Tensor& k, const RotaryArgs& a, Tensor& q
                             int32_of("tokens", t), int32_of("nheads_q", q.size(1)),
                             k.defined() ? int32_of("nheads_kv", k.size(1)) : 0,
                             int32_of("head_dim", d), stream_of(dev));
-  if (rc != ATTN_OK) throw Refused{"attn_rotary", rc};
+  if (rc != ATTN_OK) throw Refused("attn_rotary", rc);
 }
 
 // a gradient as the kernel can read it
@@ -325,6 +343,8 @@ Tensor append_run(AppendArgs& a) {
   const Rows k = rows_of("k", a.k, dev), v = rows_of("v", a.v, dev);
   if (a.v.sizes() != a.k.sizes()) bad("v must have shape ", a.k.sizes(), ", got ", a.v.sizes());
   const attn_paged_cache_t c = cache_of(a.cache, dev);
+  if (!disjoint(a.cache.k) || !disjoint(a.cache.v))
+    bad("k_cache and v_cache are written: they must not overlap themselves");
   const int64_t t = a.k.size(0), d = c.head_dim;
   if (a.k.size(1) != c.nheads_kv || a.k.size(2) != d)
     bad("k ", a.k.sizes(), " does not match the cache's ", c.nheads_kv, " heads of ", d);
@@ -351,7 +371,7 @@ Tensor append_run(AppendArgs& a) {
                             int32_of("max_seqlen", a.max_seqlen),
                             a.q.defined() ? int32_of("nheads_q", a.q.size(1)) : 0, f, nf,
                             a.interleaved, static_cast<float>(a.mscale), stream_of(dev));
-  if (rc != ATTN_OK) throw Refused{"attn_paged_append", rc};
+  if (rc != ATTN_OK) throw Refused("attn_paged_append", rc);
   return a.q_out;
 }
 
@@ -411,7 +431,7 @@ void fwd_run(FwdArgs& a) {
                          a.lse.defined() ? a.lse.data_ptr<float>() : nullptr,
                          a.workspace.defined() ? a.workspace.data_ptr() : nullptr,
                          a.workspace.defined() ? a.workspace.nbytes() : 0, stream_of(dev));
-  if (rc != ATTN_OK) throw Refused{"attn_paged_fwd", rc};
+  if (rc != ATTN_OK) throw Refused("attn_paged_fwd", rc);
 }
 
 // ---------------------------------------------------------------------------
@@ -477,7 +497,7 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
     return f();
   } catch (const PyFail&) {
   } catch (const BadValue& e) {
-    PyErr_SetString(PyExc_ValueError, e.text.c_str());
+    PyErr_SetString(PyExc_ValueError, e.what());
   } catch (const Refused& e) {
     PyObject* x = PyObject_CallFunction(attn_error, "si", e.name, e.code);
     if (x) {
@@ -521,6 +541,7 @@ PyObject* py_rotary_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 8, [&] {
     const Tensor q = tensor_of("q", a[0]), k = tensor_of("k", a[1], true);
     const RotaryArgs r = rotary_args(a, false);
+    if (r.inv_freq.requires_grad()) bad("inv_freq has no gradient here: pass it detached");
     auto opt = [](const Tensor& t) {
       return t.defined() ? std::optional<Tensor>(t) : std::nullopt;
     };

@@ -370,7 +370,10 @@ typedef struct {
  * the old scale elsewhere.  Where a scale grows, the codes already in the page
  * are moved to it (exactly, for powers of two, down to the smallest normal
  * code).  Infinities and NaN are held as NaN.
- * Two sequences of one call must not append to the same page.  Rows behind
+ * The pools and scales must not overlap themselves or one another, and two
+ * sequences of one call must not append to the same page (full pages may be
+ * shared).  A token whose position is negative or past the block table is not
+ * written; its q is rotated by that position all the same.  Rows behind
  * cu_seqlens[batch] are not read, and q_out is left as it was there.
  */
 attn_status_t attn_paged_append(const attn_paged_cache_t* cache, const void* k, int64_t k_st,
@@ -406,6 +409,10 @@ attn_status_t attn_paged_append(const attn_paged_cache_t* cache, const void* k, 
  *                  bytes for the same arguments, 256-byte aligned, clobbered;
  *                  NULL when that is 0.  Calls sharing it must not overlap on
  *                  the GPU.
+ * Scores and sums are fp32.  The weights are rounded to bf16 for the product with
+ * the values (f16 with an e4m3 cache, bf16 where its keys are packed first: 128
+ * rows of a group or more).  With an e4m3 cache and 17 to 128 rows of a group,
+ * elements of q below 2^-10 of their row's largest are held to 2^-17 of it.
  * What the slots of a page past the sequence's length hold, and the pages of
  * other sequences, NaN included, never reaches the result.
  */

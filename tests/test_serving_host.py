@@ -307,6 +307,44 @@ def test_paged_binding_refuses(case):
         assert "CUDA tensors only" not in str(e.value)
 
 
+def test_an_empty_pool_is_refused(lib):
+    assert _append(lib, _cache(pages=0)) == 1
+    assert _paged(lib, _cache(pages=0)) == 1
+
+
+def test_errors_of_a_backward_reach_the_caller(rec):
+    x = torch.zeros(5, 4, 128, dtype=BF).requires_grad_(True)
+    y, _ = ea.rotary(x, None, ea.rope_frequencies(128)[0])
+    rec.code = 3
+    with pytest.raises(RuntimeError, match="attn_rotary"):
+        y.backward(torch.zeros_like(y))
+    rec.code = 0
+    y, _ = ea.rotary(x, None, ea.rope_frequencies(128)[0])
+    y.backward(torch.zeros_like(y))
+    rec.code = 3
+    with pytest.raises(ea.AttnError):
+        ea.rotary(x, None, ea.rope_frequencies(128)[0])
+
+
+def test_a_frequency_that_wants_a_gradient_is_refused(rec):
+    f = ea.rope_frequencies(128)[0].requires_grad_(True)
+    with pytest.raises(ValueError, match="inv_freq"):
+        ea.rotary(torch.zeros(5, 4, 128, dtype=BF), None, f)
+
+
+@pytest.mark.parametrize("case", ["heads", "tokens", "pages"])
+def test_append_refuses_a_pool_that_overlaps_itself(rec, case):
+    p = _problem()
+    n, page, h, d = p["kc"].shape
+    dims = {"heads": (n, page, 1, d), "tokens": (n, 1, h, d), "pages": (1, page, h, d)}[case]
+    one = torch.zeros(dims).to(sr.E4M3).expand(n, page, h, d)
+    for kc, vc in ((one, p["vc"]), (p["kc"], one)):
+        with pytest.raises(ValueError, match="overlap"):
+            ea.attn_paged_append(p["k"], p["v"], kc, vc, p["table"], p["cu"], p["lens"], 3,
+                                 **p["kw"])
+    ea.attn_paged_fwd(p["q"], one, one, p["table"], p["cu"], p["lens"], 3, 20, **p["kw"])
+
+
 def test_cpu_tensors_are_refused():
     p = _problem()
     with pytest.raises(ValueError, match="CUDA tensors only"):
