@@ -26,7 +26,7 @@
 //         walks over the heads; the page's maximum by one redux and one shared
 //         atomic per warp.  Bound by HBM.
 // Rows whose position is negative or past the block table, and pages outside
-// the pool, are not written.
+// the pool, are not written; their queries are rotated all the same.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -73,13 +73,13 @@ struct PageSpan {
 __device__ __forceinline__ PageSpan page_span(const AppendParams& p, int b, int j) {
   PageSpan s;
   const int c0 = p.cu[b], n = p.cu[b + 1] - c0, len = p.seqlens[b];
-  const int start = len - n, lo = max(start, 0);
-  const int jp = (lo >> p.page_shift) + j;
+  const int start = len - n;
+  const int jp = (start >> p.page_shift) + j;  // below 0 for positions below 0
   s.row0 = static_cast<int64_t>(c0) - start;
-  s.first = max(lo, jp << p.page_shift);
+  s.first = max(start, jp << p.page_shift);
   s.last = min(len, (jp + 1) << p.page_shift);
   s.page = -1;
-  if (n > 0 && s.first < s.last && jp < p.pages_per_seq) {
+  if (n > 0 && s.first < s.last && jp >= 0 && jp < p.pages_per_seq) {
     const int page = p.table[b * p.table_stride + jp];
     if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) s.page = page;
   }

@@ -10,7 +10,7 @@
 // values are the second operands in shared memory, in swizzled panels (K of 64 or 128
 // bytes a key, K-major; V of 64 columns, MN-major).  bf16: both as they are.  e4m3: K's
 // codes as they are (kind::f8f6f4), against Q as the sum of two e4m3 rows, which holds
-// a bf16 exactly; V converted to f16 (exact), since a weight needs f16's range and
+// a bf16 exactly (to 2^-17 of the row's largest element); V converted to f16 (exact), since a weight needs f16's range and
 // bits.  (With K converted too the conversions, at 3 to 4 cycles a pair and scheduler,
 // set the pace.)
 //
@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(320, 1)
           reinterpret_cast<const uint4*>(p.q + w.row_index(p, live ? r : 0) * D);
       if constexpr (FP8) {
         // scaled so that the largest element is in [2^7, 2^8), and as a sum of two codes:
-        // 4 significant bits, then the rest; exact for elements down to 2^-10 of that
+        // 4 significant bits, then the rest; exact for elements down to 2^-10 of that, and
+        // smaller ones are off by at most half the least code, 2^-17 of the largest
         uint32_t m = 0;
 #pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {

@@ -164,6 +164,31 @@ def test_append_views_and_queries_in_place():
         assert same_codes(a[0], b[0]) and same_codes(a[1], b[1])
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_with_more_new_tokens_than_the_length(e4m3):
+    # positions -7 .. 12 and -3 .. 0: the tokens before position 0 go nowhere, the
+    # queries are rotated by their positions in both kernels
+    d, page, hkv, n, lens = 64, 16, 2, [20, 4], [13, 1]
+    cu = cu_of(n)
+    f = ea.rope_frequencies(d)[0].cuda()
+    k, q = rows(24, hkv, d, 71).cuda(), rows(24, 4, d, 72).cuda()
+    off = i32([x - y for x, y in zip(lens, n)])
+    want = ea.attn_rotary(q, None, f, cu_seqlens=i32(cu), offsets=off)[0]
+    kr = ea.attn_rotary(k, None, f, cu_seqlens=i32(cu), offsets=off)[0].cpu()
+    c = Cache([0, 0], lens, hkv, d, page, e4m3, seed=7)
+    sr.append(kr, c.k, c.k_scale, c.table, cu, lens)
+    for j in (0, 1):  # the sequences together (20 new tokens), and the second alone (4)
+        c2 = Cache([0, 0], lens, hkv, d, page, e4m3, seed=7)
+        kc, vc, table, kw = c2.to("cuda")
+        a = cu[j]
+        got = ea.attn_paged_append(k[a:], k[a:], kc, vc, table[j:], i32([x - a for x in cu[j:]]),
+                                   i32(lens[j:]), max(n[j:]), q=q[a:], inv_freq=f, **kw)
+        assert torch.equal(got, want[a:])
+        for b in range(j, 2):
+            at = int(c.table[b, 0])
+            assert same_codes(kc[at].cpu(), c.k[at])
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
@@ -515,3 +540,148 @@ def test_prompt_chunks_and_single_rows_agree():
                                  i32([220 + i]), 20, 1000, causal=True, **{
                                      k: v for k, v in kw.items()})
         assert float((part[1] - whole[1][:, i:i + 20]).abs().max()) <= 2 * LSE_TOL
+
+
+# ---------------------------------------------------------------------------
+# 9 rows of a group and more over the pages themselves
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("most", [9, 16, 17, 33, 64, 65, 127, 128, 129, 300])
+def test_rows_of_a_group(d, e4m3, most):
+    # each number of rows a CTA can hold, one below and above it, and several row tiles
+    page = {64: 16, 128: 64, 256: 128}[d]
+    n, lens = [most, 0, 2, 1], [most + 200, 50, 131, 640]
+    c = Cache(lens, lens, 1, d, page, e4m3, seed=most, junk=math.nan, head_major=most % 2 == 0)
+    q = rows(sum(n) + 2, 1, d, 600 + most, 0.3)
+    attend(c, q, n, hq=1, causal=True, splits=1)
+    attend(c, q, n, hq=1, window=(130, 40), softcap=15.0, splits=4)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_rows_of_a_group_and_every_page(page, e4m3):
+    # parts begin at any page, lengths end inside a tile, a page and a 16-key block
+    n, lens = [5, 4, 5, 3, 1], [1000, 383, 129, 5, 64]
+    for d, head_major in ((64, False), (128, True), (256, False)):
+        c = Cache(lens, lens, 2, d, page, e4m3, seed=page, junk=math.nan, head_major=head_major)
+        q = rows(sum(n), 10, d, 620, 0.3)
+        for splits, window in ((1, None), (3, None), (7, (300, 10))):
+            attend(c, q, n, hq=10, causal=window is None, window=window, splits=splits)
+
+
+def test_queries_of_uneven_size():
+    # one element far above the others of its row: the small ones decide the scores too
+    d, n, lens = 128, [20], [500]
+    c = Cache(lens, lens, 1, d, 64, True, seed=31)
+    c.k[:, :, :, 5] = 0.0
+    q = rows(20, 1, d, 630, 0.0)
+    q[:, :, 5] = 256.0
+    cu = [0, 20]
+    kc, vc, table, kw = c.to("cuda")
+    out, lse = ea.attn_paged_fwd(q.cuda(), kc, vc, table, i32(cu), i32(lens), 20, 500,
+                                 num_splits=1, **kw)
+    ref, ref_lse, pabs = sr.attend(q, c.k, c.v, c.k_scale, c.v_scale, c.table, cu, lens, d ** -0.5)
+    # an element of q is off by at most 2^-17 of 256, so a score by at most
+    # e = 2^-9 d^-1/2 max_j sum |k_j|, a weight by the factor exp(2 e) and O by that
+    # much of sum p |v|, beyond the bound of the other roundings
+    keys = sr.keys_of(c.k, c.k_scale, c.table[0], 500)
+    e = 2.0 ** -9 * d ** -0.5 * float(keys.abs().sum(-1).max())
+    err = (out.cpu().double() - ref).abs()
+    assert bool((err <= sr.o_bound(ref, pabs, True) + math.expm1(2 * e) * pabs).all())
+    assert float((lse.cpu().double() - ref_lse).abs().max()) <= LSE_TOL + e
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [1, 6, 30])
+def test_heads_that_share_memory(e4m3, n):
+    # a pool of one head seen as four (stride 0) gives what four copies give
+    d, page, lens = 128, 32, [200]
+    c = Cache(lens, lens, 1, d, page, e4m3, seed=41)
+    kc, vc, table, kw = c.to("cuda")
+    many = {k: v.expand(-1, 4).contiguous() for k, v in kw.items()}
+    q = rows(n, 16, d, 640, 0.3).cuda()
+    args = (table, i32([0, n]), i32(lens), n, 200)
+    want = ea.attn_paged_fwd(q, kc.expand(-1, -1, 4, -1).contiguous(),
+                             vc.expand(-1, -1, 4, -1).contiguous(), *args, num_splits=2, **many)
+    got = ea.attn_paged_fwd(q, kc.expand(-1, -1, 4, -1), vc.expand(-1, -1, 4, -1), *args,
+                            num_splits=2, **many)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+@pytest.mark.parametrize("d,n", [(128, 1), (128, 4), (128, 12), (256, 5), (64, 100)])
+def test_two_streams_and_a_graph(d, n):
+    # calls at once on two streams, each with its own workspace, and a captured call
+    # replayed after its inputs changed
+    lens = [700, 900]
+    cu = i32([0, n, 2 * n])
+    sides, pools, qs, want = [torch.cuda.Stream() for _ in range(2)], [], [], []
+    for i in range(2):
+        c = Cache(lens, lens, 2, d, 64, True, seed=50 + i)
+        pools.append(c.to("cuda"))
+        qs.append(rows(2 * n, 8, d, 650 + i, 0.3).cuda())
+
+    def call(i):
+        kc, vc, table, kw = pools[i]
+        return ea.attn_paged_fwd(qs[i], kc, vc, table, cu, i32lens, n, 900, causal=True, **kw)
+
+    i32lens = i32(lens)
+    want = [call(i) for i in range(2)]
+    for side in sides:
+        side.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(5):
+        for i, side in enumerate(sides):
+            with torch.cuda.stream(side):
+                got[i].append(call(i))
+    for side in sides:
+        torch.cuda.current_stream().wait_stream(side)
+    for i in range(2):
+        for g in got[i]:
+            assert torch.equal(g[0], want[i][0]) and torch.equal(g[1], want[i][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g = call(0)
+    qs[0].copy_(rows(2 * n, 8, d, 660, 0.3))
+    i32lens -= 37
+    graph.replay()
+    again = call(0)
+    assert torch.equal(g[0], again[0]) and torch.equal(g[1], again[1])
+
+
+@pytest.mark.parametrize("n", [1, 5, 20, 200])
+def test_rows_of_no_sequence_stay(n):
+    # a batch padded behind its last sequence: those rows are neither read nor written
+    d, lens = 128, [600, 300]
+    c = Cache(lens, lens, 2, d, 64, True, seed=61)
+    kc, vc, table, kw = c.to("cuda")
+    q = rows(2 * n + 7, 8, d, 670, 0.3)
+    q[2 * n:] = math.nan
+    for splits in (0, 1, 3):
+        out = torch.full_like(q, 3.0).cuda()
+        lse = torch.full((8, 2 * n + 7), 3.0, device="cuda")
+        ea.attn_paged_fwd(q.cuda(), kc, vc, table, i32([0, n, 2 * n]), i32(lens), n, 600, out=out,
+                          lse=lse, num_splits=splits, **kw)
+        assert bool((out[2 * n:] == 3).all()) and bool((lse[:, 2 * n:] == 3).all())
+        assert bool(torch.isfinite(out).all())
+
+
+def test_rows_of_a_group_in_a_pool_past_32_bits():
+    d, page, hkv, n = 128, 64, 8, 12
+    pages = (1 << 31) // (page * hkv * d) + 2000
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("not enough memory")
+    dev = torch.device("cuda")
+    c = Cache([300], [300], hkv, d, page, True, seed=71, spare=0)
+    kc = torch.zeros(pages, hkv, page, d, dtype=sr.E4M3, device=dev).transpose(1, 2)
+    vc = torch.zeros_like(kc)
+    ks, vs = (torch.ones(pages, hkv, device=dev) for _ in range(2))
+    for i in range(c.pages):
+        at = pages - 1 - i
+        kc[at], vc[at], ks[at], vs[at] = (x[i].to(dev) for x in (c.k, c.v, c.k_scale, c.v_scale))
+    q = rows(n, 32, d, 680, 0.2)
+    out, lse = ea.attn_paged_fwd(q.cuda(), kc, vc, (pages - 1 - c.table).to(dev), i32([0, n]),
+                                 i32([300]), n, 300, causal=True, k_scale=ks, v_scale=vs)
+    ref = sr.attend(q, c.k, c.v, c.k_scale, c.v_scale, c.table, [0, n], [300], d ** -0.5,
+                    causal=True)
+    compare(out, lse, *ref, True)

@@ -186,3 +186,25 @@ def test_in_a_graph_and_on_another_stream():
     q.copy_(rows(t, 4, d, 22))
     graph.replay()
     assert torch.equal(got[0], ea.attn_rotary(q, k, f)[0]) and torch.equal(got[1], want[1])
+
+
+def test_gradient_in_a_graph_beside_an_eager_one():
+    # forward and backward captured while an eager graph of the same leaves lives
+    t, d = 130, 128
+    f = ea.rope_frequencies(d)[0].cuda()
+    q, k = (rows(t, h, d, 30 + h).cuda().requires_grad_(True) for h in (4, 2))
+    g = [rows(t, h, d, 40 + h).cuda() for h in (4, 2)]
+    eager = ea.rotary(q, k, f)
+    want = torch.autograd.grad(eager, (q, k), g, retain_graph=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ea.rotary(q, k, f)
+        got = torch.autograd.grad(out, (q, k), g)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    for x in g:
+        x.neg_()
+    graph.replay()
+    assert all(torch.equal(-a, b) for a, b in zip(want, got))
+    again = torch.autograd.grad(eager, (q, k), g)
+    assert all(torch.equal(a, b) for a, b in zip(again, got))
