@@ -101,7 +101,10 @@ def attn_rotary(q, k, inv_freq, *, cu_seqlens=None, offsets=None, positions=None
 
 def rotary(q, k, inv_freq, *, cu_seqlens=None, offsets=None, positions=None, interleaved=False,
            mscale=1.0):
-    """Differentiable attn_rotary: the gradient is the inverse rotation."""
+    """Differentiable attn_rotary: the gradient, of q and k, is the inverse rotation.
+
+    A backward can be captured into a CUDA graph when no eager graph of the same
+    leaves is alive (torch refuses the capture otherwise)."""
     return (_binding or _load()).rotary_grad(q, k, inv_freq, cu_seqlens, offsets, positions,
                                              interleaved, mscale)
 
@@ -118,7 +121,7 @@ def attn_paged_append(k, v, k_cache, v_cache, block_table, cu_seqlens, seqlens_k
     An e4m3 cache is written under one power-of-two scale per page and head,
     which grows as larger values arrive (see attn_paged_append in attn.h); the
     scales are updated in place.  ``q_out`` may be q; rows behind the last
-    sequence are left as they were."""
+    sequence are left as they were (undefined in an output made here)."""
     return (_binding or _load()).append(k, v, k_cache, v_cache, block_table, cu_seqlens, seqlens_k,
                                         max_seqlen, k_scale, v_scale, q, q_out, inv_freq,
                                         interleaved, mscale)
