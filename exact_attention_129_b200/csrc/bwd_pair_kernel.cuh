@@ -338,7 +338,11 @@ __device__ __forceinline__ void pair_mma_b(const BwdTile& t, const PairSmem& s, 
     const int b = j & 1;
     // the tile from the peer: dS^T (rank 0) or P^T (rank 1), by bulk copy
     uint64_t* rx_full = rank == 0 ? &s.xb_full[b] : &s.xa_full[b];
-    if (!w.warp(rx_full, (j >> 1) & 1, ERR_BWDP_MMA | 5)) {
+    // and the stage: dS^T comes after S, which has waited for Q, but P^T may come
+    // before dO of its block has landed (the stage stays until this warp has read it,
+    // so the phase cannot pass)
+    if (!w.warp(rx_full, (j >> 1) & 1, ERR_BWDP_MMA | 5) ||
+        !w.warp(&s.st_full[r.slot], r.phase, ERR_BWDP_MMA | 8)) {
       ok = false;
       break;
     }
