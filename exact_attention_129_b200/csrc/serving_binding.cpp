@@ -239,10 +239,18 @@ struct RotaryNode : public torch::autograd::Function<RotaryNode> {
     auto opt = [](const Tensor& t) {
       return t.defined() ? std::optional<Tensor>(t) : std::nullopt;
     };
-    auto turn = [&](const Tensor& q, const std::optional<Tensor>& k) {
-      return apply(q, k, saved[0], opt(saved[1]), opt(saved[2]), opt(saved[3]),
-                   ctx->saved_data["interleaved"].toBool(), !ctx->saved_data["inverse"].toBool(),
-                   ctx->saved_data["mscale"].toDouble());
+    const bool interleaved = ctx->saved_data["interleaved"].toBool();
+    const bool inverse = !ctx->saved_data["inverse"].toBool();
+    const double mscale = ctx->saved_data["mscale"].toDouble();
+    auto turn = [&](const Tensor& q,
+                    const std::optional<Tensor>& k) -> torch::autograd::variable_list {
+      if (at::GradMode::is_enabled())  // a gradient of the gradient is wanted
+        return apply(q, k, saved[0], opt(saved[1]), opt(saved[2]), opt(saved[3]), interleaved,
+                     inverse, mscale);
+      Tensor qo, ko;
+      rotary_run(q, k.value_or(Tensor()),
+                 {saved[0], saved[1], saved[2], saved[3], interleaved, inverse, mscale}, qo, ko);
+      return {qo, ko};
     };
     Tensor dq, dk;
     const bool want_q = ctx->needs_input_grad(0) && grads[0].defined();
