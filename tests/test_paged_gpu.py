@@ -685,3 +685,29 @@ def test_rows_of_a_group_in_a_pool_past_32_bits():
     ref = sr.attend(q, c.k, c.v, c.k_scale, c.v_scale, c.table, [0, n], [300], d ** -0.5,
                     causal=True)
     compare(out, lse, *ref, True)
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (256, 128)])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [1, 4, 10, 40, 100])
+def test_pages_outside_the_pool(d, page, e4m3, n):
+    # table entries that name no page of the pool read as pages of zeros, in every kernel
+    lens = [400, 300]
+    c = Cache(lens, lens, 2, d, page, e4m3, seed=81)
+    used = {int(x) for b, m in enumerate(lens) for x in c.table[b, :-(-m // page)]}
+    empty = next(i for i in range(c.pages) if i not in used)
+    c.k[empty], c.v[empty] = 0, 0
+    if e4m3:
+        c.k_scale[empty] = c.v_scale[empty] = 1.0
+    q = rows(2 * n, 4, d, 690 + n, 0.3)
+    kc, vc, table, kw = c.to("cuda")
+    for (b, j), name in zip(((0, 1), (0, 0), (1, 2)), (10 ** 7, -1, c.pages)):
+        table[b, j] = name
+        c.table[b, j] = empty
+    for splits in (0, 1, 3):
+        out, lse = ea.attn_paged_fwd(q.cuda(), kc, vc, table, i32([0, n, 2 * n]), i32(lens), n,
+                                     400, causal=True, num_splits=splits, **kw)
+        ref = sr.attend(q, c.k, c.v, c.k_scale, c.v_scale, c.table, [0, n, 2 * n], lens,
+                        d ** -0.5, causal=True)
+        # P in f16 except where an unsplit call of many rows packs its keys (see attend())
+        compare(out, lse, *ref, e4m3 and (splits != 0 or 2 * n < 128))
