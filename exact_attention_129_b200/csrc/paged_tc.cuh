@@ -30,7 +30,10 @@
 // What bounds it: a tile's chain.  Softmax of a tile about 1200 cycles for 32 keys a
 // thread (its scheduler runs one softmax and one conversion warp), then 250 for the
 // signal to the MMA warp, 150 + 540 for P V, 250 + 450 for S of the tile after the next,
-// which needs the slot: about 1500 cycles a tile, whatever its size.  One CTA alone, 32
+// which needs the slot: about 1500 cycles a tile, whatever its size.  (head_dim 256: the
+// 16 MMAs of 64 keys for S take about 50 cycles each, a full-rate one would take 16; with
+// P V they fill 1400 of the 1500.)  P V from a warp of its own, or the zero weights
+// written before the softmax, changed nothing.  One CTA alone, 32
 // rows, e4m3: 7.6, 9.2 and 17 ns a key of head_dim 64, 128, 256; bf16 6.0, 7.7, 14.2,
 // where 512 CTAs run at 4.4, 5.8 and 6.2 TB/s.  More CTAs an SM (smaller tiles, one slot
 // of S) gave 41 ns a key of 512 CTAs of e4m3 and head_dim 128, one CTA with these 38.
