@@ -230,8 +230,8 @@ struct PagedShape {
 };
 
 constexpr double kRoundNs[2] = {3000.0, 6000.0};  // a CTA's set-up and drain: mma.sync, tcgen05
-constexpr double kEqualBatches = 0.35;
-constexpr double kSpread = 0.1;  // of the time of a CTA
+constexpr double kEqualBatches = 0.45;
+constexpr double kSpread[2] = {0.2, 0.0};  // of a CTA's time: three on an SM, or one
 constexpr double kMergeCopies = 2.0;  // the parts of O cross HBM or L2 about so often
 
 // one round of k CTAs of chunk keys side by side
@@ -272,18 +272,20 @@ double paged_plan_tiles(const PagedShape& x, int want, int sms, PagedPlan* pl) {
   for (int s = want ? want : 1; s <= (want ? want : kPagedMaxSplits); s += 1 + s / 8) {
     const int64_t chunk = chunk_of(s), parts = (x.span + chunk - 1) / chunk;
     const double c = static_cast<double>(chunk);
-    // max_k bounds the lengths, which are not known here: as if a third of the batches
-    // were of equal sequences and the others of sequences of 0.6 of it on average.  (Half
-    // and half: 32 equal sequences of 4K with 8 rows stay in one part, 55 us, instead of
-    // two, 69; 128 ragged ones of up to 8K go from four parts to two, 319 to 341 us.)
+    // max_k bounds the lengths, which are not known here: as if nearly half of the batches
+    // were of equal sequences and the others of sequences of 0.6 of it on average.  (0.35
+    // against 0.45: 32 equal sequences of 4K with 8 rows 69 and 59 us, 128 ragged ones of up
+    // to 8K 312 and 314.)
     const int64_t n = per_part * parts;
     double t = rounds_ns(n, slots, c, key, x.key_bytes, fixed);
     if (x.batch > 1)
       t = kEqualBatches * t +
           (1. - kEqualBatches) * ragged_ns(0.6 * n, slots, c, key, x.key_bytes, fixed);
     // CTAs side by side do not end together: 16 sequences of 64K take 334 us with one
-    // long CTA per slot when all goes well, 356 to 390 in most runs, with 16 parts 337 to 375
-    t += 4000. + kSpread * round_ns(std::min(n, slots), c, key, x.key_bytes, 0.);
+    // long CTA per slot when all goes well, 356 to 390 in most runs, with 16 parts 333 to
+    // 375.  (The tcgen05 kernel, alone on its SM, does not gain: drafts 74 us without
+    // this term, 88 with 0.2.)
+    t += 4000. + kSpread[ri > 1] * round_ns(std::min(n, slots), c, key, x.key_bytes, 0.);
     if (parts > 1)
       t += 2000. + kMergeCopies * 8. * parts * x.total_q * x.hq * x.d / kHbmBytesPerNs;
     if (!splits || t < best) best = t, splits = parts;
