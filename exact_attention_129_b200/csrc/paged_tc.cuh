@@ -91,13 +91,17 @@ struct PagedTcCfg {
   static constexpr int OUT_ROW = 68;         // floats: a chunk of 64 columns of O at the end
   static constexpr int OUT = 128 * OUT_ROW * 4;
   static constexpr int BAR_OFF = TILES_END > OUT ? TILES_END : OUT;
-  static constexpr int FLAG_OFF = BAR_OFF + 192;               // [NBUF] ints, abort, tmem
+  static constexpr int FLAG_OFF = BAR_OFF + 192;  // [NBUF][4] bytes of the V warps, abort, tmem
   static constexpr int ML_OFF = FLAG_OFF + 32;                 // [128] m, l
   static constexpr int BAD_OFF = ML_OFF + 128 * 8;             // [NBUF][2][BK][WORDS]
   static constexpr int SEEN_OFF = BAD_OFF + NBUF * 2 * BK * WORDS * 4;  // [2][128][WORDS]
   static constexpr int USED = SEEN_OFF + 2 * 128 * WORDS * 4 + 1024;  // 1024-byte alignment
   // one CTA an SM: a second one would wait for tensor memory
   static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
+  // the 128 threads of warps 4-7 take pieces of 16 bytes; a warp's are of whole keys, so
+  // that what is noted of a key (BAD_OFF) belongs to one warp
+  static constexpr int CPR = D * ESZ / 16;
+  static_assert(32 % CPR == 0 && BK % (128 / CPR) == 0);
   static constexpr float OFFSET = FP8 ? 6.f : 0.f;
   static constexpr float RAISE = 8.f + OFFSET;
   static constexpr uint32_t FORMAT = FP8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // f16: zeros
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(320, 1)
   uint64_t* used = ready + NBUF;     // [NBUF] e4m3: P V is done
   uint64_t* s_full = used + NBUF;    // [2] a slot holds S,
   uint64_t* p_full = s_full + 2;     // [2] or P
-  int* tile_bad = reinterpret_cast<int*>(smem + C::FLAG_OFF);         // [NBUF]
+  int* tile_bad = reinterpret_cast<int*>(smem + C::FLAG_OFF);  // [NBUF], a byte of each V warp
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF + 16);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(smem + C::FLAG_OFF + 20);
   float2* ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
@@ -588,16 +592,24 @@ __global__ void __launch_bounds__(320, 1)
   } else if (warp < 8) {
     // ---------------------------------------------------- V for the MMAs (bf16: checked)
     const int lt = tid - 128;
-    constexpr int CPR = D * C::ESZ / 16;       // 16-byte pieces of a key's row
+    constexpr int CPR = C::CPR;                // 16-byte pieces of a key's row
     constexpr int STEP = 128 / CPR;            // keys between a thread's pieces
     constexpr int N = BK / STEP;               // pieces of a thread and tile
     const int piece = lt % CPR, row0 = lt / CPR;
     // a tile with keys that only some rows see: values that are not finite are noted
-    // and replaced by zeros, because a zero weight would not hide them
+    // and replaced by zeros, because a zero weight would not hide them.  Each warp clears
+    // the words of its own keys (CPR | 32) and has a flag byte of its own: a barrier of
+    // the four warps here could wait for one that has given up.
+    uint8_t* flags = reinterpret_cast<uint8_t*>(tile_bad) + (warp - 4);  // of buffer b at 4 b
     auto clear_bad = [&](int b) {
-      for (int i = lt; i < 2 * BK * WORDS; i += 128) bad[b * 2 * BK * WORDS + i] = 0;
-      if (lt == 0) tile_bad[b] = 0;
-      named_bar_sync(3, 128);
+      constexpr int KEYS = 32 / CPR;  // of a warp and step
+      for (int i = lane; i < 2 * N * KEYS * WORDS; i += 32) {
+        const int word = i % WORDS, k = i / WORDS % (N * KEYS), sign = i / (WORDS * N * KEYS);
+        const int key = k / KEYS * STEP + (warp - 4) * KEYS + k % KEYS;
+        bad[((b * 2 + sign) * BK + key) * WORDS + word] = 0;
+      }
+      if (lane == 0) flags[4 * b] = 0;
+      __syncwarp();
     };
     auto clean = [&](int b, int key, int d0, uint32_t (&x)[4]) {  // 8 columns from d0
       uint32_t plus, minus;
@@ -605,7 +617,7 @@ __global__ void __launch_bounds__(320, 1)
       if (plus | minus) {
         atomicOr(&bad[((b * 2 + 0) * BK + key) * WORDS + d0 / 32], plus << (d0 & 31));
         atomicOr(&bad[((b * 2 + 1) * BK + key) * WORDS + d0 / 32], minus << (d0 & 31));
-        tile_bad[b] = 1;
+        flags[4 * b] = 1;
       }
     };
     for (int t = 0; t < tiles; ++t) {
