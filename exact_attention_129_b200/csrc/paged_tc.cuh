@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(320, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_at;
+  int issued = 0;  // warp 9: tiles whose loads were issued
   auto mixed = [&](int t) {  // some key of the tile is seen by some rows only
     return kb + t * BK < w.in_lo || min(kb + t * BK + BK, ke) > w.in_hi;
   };
@@ -713,9 +714,7 @@ __global__ void __launch_bounds__(320, 1)
       }
       __syncwarp();
     }
-    if (t < tiles)  // gave up: the copies under way land before the memory goes
-      for (int u = max(0, t - STAGES); u < t; ++u)
-        mbar_wait_drain(&landed[u % STAGES], (u / STAGES) & 1, tp.timeout_ns);
+    issued = t;
   } else {
     // ------------------------------------------------------------------- MMAs
     named_bar_sync(1, 160);
@@ -771,16 +770,23 @@ __global__ void __launch_bounds__(320, 1)
                (t | k) != 0);
       mma_commit(FP8 ? &used[b] : &left[b]);
     }
-    // a CTA that gave up: what was issued has to end before its memory goes
-    if (*abort) {
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 100000) {  // 100 us, far above any tile's MMAs
-      }
-    }
     tc_fence_before();
   }
   __syncthreads();
   tc_fence_after();
+  if (*abort) {
+    // A CTA that gave up, in whichever warp: the copies and MMAs that were issued have to
+    // end before its memory goes.  (Known here for all warps: the loads and the MMAs of
+    // a warp that went through may still be under way when another one's wait ran out.)
+    if (warp == 9)
+      for (int u = max(0, issued - STAGES); u < issued; ++u)
+        mbar_wait_drain(&landed[u % STAGES], (u / STAGES) & 1, tp.timeout_ns);
+    if (warp == 8) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 100000) {  // 100 us, far above any tile's MMAs
+      }
+    }
+  }
   if (warp == 8) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 

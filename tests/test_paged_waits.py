@@ -75,3 +75,29 @@ def test_the_words_a_warp_clears_are_those_it_notes(d, esz):
             key = lt // cpr + i * step
             for col in range(lt % cpr * (16 // esz), (lt % cpr + 1) * (16 // esz)):
                 assert cleared[0, key, col // 32] == cleared[1, key, col // 32] == lt // 32
+
+
+def test_copies_and_mmas_end_before_their_memory_goes():
+    # another warp's wait can run out after the loading warp or the MMA warp has gone
+    # through its tiles: only behind the block's last barrier is it known whether one did
+    src = kernel()
+    last = src.rindex("__syncthreads()")
+    for role in roles()[2:]:
+        assert "drain" not in role and "*abort" not in role
+    tail = src[last:]
+    gave_up = braces(tail, tail.index("if (*abort)"))
+    assert "mbar_wait_drain(&landed[u % STAGES], (u / STAGES) & 1" in gave_up
+    assert "max(0, issued - STAGES)" in gave_up and "globaltimer_ns() - t0 < " in gave_up
+    assert tail.index("if (*abort)") < tail.index("tmem_dealloc")
+
+
+@pytest.mark.parametrize("stages", [3, 4])
+@pytest.mark.parametrize("issued", [0, 1, 2, 3, 4, 5, 11])
+def test_the_drain_waits_for_the_last_phase_of_every_stage(stages, issued):
+    # mbarrier phases count from 0 per stage; waiting for the parity of a phase that is
+    # done, or whose successor has begun and is not done, returns
+    last = {}
+    for t in range(issued):
+        last[t % stages] = t // stages
+    waits = {u % stages: (u // stages) & 1 for u in range(max(0, issued - stages), issued)}
+    assert waits == {s: phase & 1 for s, phase in last.items()}
