@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "attn.h"
 #include "paged_append.cuh"
@@ -299,25 +300,37 @@ double paged_plan_tiles(const PagedShape& x, int want, int sms, PagedPlan* pl) {
   return best;
 }
 
-// false: not open for this call
-bool paged_plan_dense(const PagedShape& x, int hkv, int sms, double limit, PagedPlan* pl) {
+// ATTN_PAGED_PACK=0: the packed copies are not used; 1: they are, for any number of rows
+// and num_splits, wherever their sizes fit.  Read on every call, for tests and for
+// callers without the memory.  -1: not set
+int paged_pack_switch() {
+  const char* e = std::getenv("ATTN_PAGED_PACK");
+  return !e ? -1 : e[0] == '0' ? 0 : e[0] == '1' ? 1 : -1;
+}
+
+// false: not open for this call, or no quicker than `limit`; forced: whatever the estimate
+bool paged_plan_dense(const PagedShape& x, int hkv, int sms, int want, double limit, bool forced,
+                      PagedPlan* pl) {
   const int64_t key_rows = x.batch * (x.max_k + kGatherPad);
   const int64_t copy = key_rows * hkv * x.d * 2;
-  if (x.rows < 128 || x.batch > 32767 || 2 * copy > kDenseBytes || key_rows >= (1 << 30))
-    return false;
+  if (x.batch > 32767 || 2 * copy > kDenseBytes || key_rows >= (1 << 30)) return false;
+  if (!forced && (x.rows < 128 || x.max_k < 512)) return false;
   // code read, copy written and read; three launches more
   const double gather = 16000. + key_rows * hkv * (x.key_bytes + 8. * x.d) / kHbmBytesPerNs;
   const int64_t tile = x.d == 256 ? 128 : 256;
   const int64_t ctas = x.units * ((x.rows + tile - 1) / tile);
   double best = 0;
   int splits = 0;
-  for (int s = 1; s <= 16 && x.max_k >= 512 * s; s *= 2) {
+  const int first = want ? want : 1, most = want ? want : 16;
+  // (attn_fwd's grid: segments times parts)
+  for (int s = first; s <= most && 2 * x.batch * s <= 65535 && (s == first || x.max_k >= 512 * s);
+       s *= 2) {
     double t = gather + rounds_ns(ctas * s, sms, static_cast<double>(x.span) / s,
                                   kDenseNsPerKey[x.d_index], 0.0, kRoundNs[0]);
     if (s > 1) t += 4000. + kMergeCopies * 8. * s * x.total_q * x.hq * x.d / kHbmBytesPerNs;
     if (!splits || t < best) best = t, splits = s;
   }
-  if (!splits || best >= limit) return false;
+  if (!splits || (!forced && best >= limit)) return false;
   pl->dense = true;
   pl->splits = splits;
   pl->key_rows = key_rows;
@@ -357,7 +370,10 @@ PagedPlan paged_plan(const attn_paged_cache_t* c, int batch, int total_q, int ma
   x.span = std::max<int64_t>(x.span, 1);
   const double t = paged_plan_tiles(x, want, sms, &pl);
   PagedPlan dense{};
-  if (want == 0 && paged_plan_dense(x, c->nheads_kv, sms, t, &dense)) return dense;
+  const int pack = paged_pack_switch();
+  if ((pack < 0 ? want == 0 : pack) &&
+      paged_plan_dense(x, c->nheads_kv, sms, want, t, pack == 1, &dense))
+    return dense;
   return pl;
 }
 

@@ -147,7 +147,8 @@ def attn_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k, ma
     ``window`` its query rows are the last ones.  ``scale``, ``window`` and
     ``softcap`` are as in attn_fwd.  ``num_splits`` 0 lets the library cut the keys
     into parts; ``workspace`` (at least paged_workspace_size bytes) is allocated
-    if None."""
+    if None.  With ``num_splits`` 0 and many rows it may hold bf16 copies of all keys
+    and values (up to 4 GiB): any other number avoids them."""
     return (_binding or _load()).fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seqlens_k,
                                      max_seqlen_q, max_seqlen_k, k_scale, v_scale, scale, causal,
                                      window, softcap, return_lse, out, lse, num_splits, workspace)

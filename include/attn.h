@@ -408,7 +408,9 @@ attn_status_t attn_paged_append(const attn_paged_cache_t* cache, const void* k, 
  *   workspace      device memory of at least attn_paged_workspace_size(...)
  *                  bytes for the same arguments, 256-byte aligned, clobbered;
  *                  NULL when that is 0.  Calls sharing it must not overlap on
- *                  the GPU.
+ *                  the GPU.  With num_splits 0 and 128 rows of a group or more it
+ *                  may hold bf16 copies of all keys and values, up to 4 GiB; any
+ *                  other num_splits needs the parts of O alone.
  * Scores and sums are fp32.  The weights are rounded to bf16 for the product with
  * the values (f16 with an e4m3 cache, bf16 where its keys are packed first: 128
  * rows of a group or more).  With an e4m3 cache and 17 to 128 rows of a group,
