@@ -591,18 +591,18 @@ attn_status_t fwd_impl(const void* q, const void* k, const void* v, const int32_
     switch (head_dim) {
       case 64:
         attn_fwd_combine_kernel<64><<<blocks, 256, 0, s>>>(
-            p.o_part, p.lse_part, static_cast<uint16_t*>(out), lse, total_q, nheads_q,
-            num_splits, return_lse);
+            p.o_part, p.lse_part, static_cast<uint16_t*>(out), lse, p.cu_q, batch, total_q,
+            nheads_q, num_splits, return_lse);
         break;
       case 128:
         attn_fwd_combine_kernel<128><<<blocks, 256, 0, s>>>(
-            p.o_part, p.lse_part, static_cast<uint16_t*>(out), lse, total_q, nheads_q,
-            num_splits, return_lse);
+            p.o_part, p.lse_part, static_cast<uint16_t*>(out), lse, p.cu_q, batch, total_q,
+            nheads_q, num_splits, return_lse);
         break;
       default:
         attn_fwd_combine_kernel<256><<<blocks, 256, 0, s>>>(
-            p.o_part, p.lse_part, static_cast<uint16_t*>(out), lse, total_q, nheads_q,
-            num_splits, return_lse);
+            p.o_part, p.lse_part, static_cast<uint16_t*>(out), lse, p.cu_q, batch, total_q,
+            nheads_q, num_splits, return_lse);
     }
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   };

@@ -1408,18 +1408,21 @@ __global__ void __launch_bounds__(FwdCfg<D>::THREADS, 1)
 // merges the SplitKV partial results).  Split s of a row holds O_s (normalised
 // over its own keys) and LSE_s; over all splits LSE = log sum_s exp(LSE_s) and
 // O = sum_s exp(LSE_s - LSE) O_s.  One warp per (row, head); a row whose
-// splits all saw no key gets O = 0 and LSE = -inf.  HBM-bound.
+// splits all saw no key gets O = 0 and LSE = -inf; rows of no segment (a batch
+// padded behind its last one) are left as they were.  HBM-bound.
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(256)
     attn_fwd_combine_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_part,
-                            uint16_t* __restrict__ out, float* __restrict__ lse, int total_q,
+                            uint16_t* __restrict__ out, float* __restrict__ lse,
+                            const int32_t* __restrict__ cu_q, int batch, int total_q,
                             int nheads_q, int num_splits, int return_lse) {
   constexpr int VPL = D / 32;  // columns per lane: 2, 4 or 8
   const long long w = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (w >= static_cast<long long>(total_q) * nheads_q) return;  // whole warps leave together
   const int row = static_cast<int>(w / nheads_q), h = static_cast<int>(w % nheads_q);
+  if (row < cu_q[0] || row >= cu_q[batch]) return;  // of no segment: no part was written
   auto lse_of = [&](int sp) {
     return lse_part[(static_cast<size_t>(sp) * nheads_q + h) * total_q + row];
   };

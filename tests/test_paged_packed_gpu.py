@@ -149,6 +149,21 @@ def test_pages_outside_the_pool(pack, d, page, e4m3):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("splits", [0, 1, 2, 7])
+def test_rows_of_no_sequence_stay(pack, d, splits):
+    # a batch padded behind its last sequence: those rows are neither read nor written, in
+    # one part or several
+    n, lens = [140, 3], [600, 300]
+    c = Cache(lens, lens, 2, d, 64, True, seed=61)
+    q = rows(sum(n) + 9, 8, d, 670, 0.3)
+    q[sum(n):] = math.nan
+    out, lse = check(c, q, n, hq=8, splits=splits, causal=True)
+    # the sentinels of guarded_empty
+    assert bool((out[sum(n):].view(torch.int16) == 0x7FC1).all())
+    assert bool((lse[:, sum(n):].view(torch.int32) == 0x7FC00001).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 def test_two_streams_and_a_graph(pack, d):
     # calls at once on two streams, each with its own workspace; a captured call replayed
     # after its inputs changed; each call gives the same bits every time
