@@ -38,6 +38,7 @@ struct PagedParams {
   int hi_off, lo_off;      // as in FwdParams, kPagedNoBound: none
   int num_splits, chunk, row_tiles;
   uint32_t k_page, k_token, v_page, v_token;  // strides in bytes
+  const int32_t* only;  // [batch]: sequences with 0 are left out; null: none is
 };
 
 // keys of sequence b: what its row of the block table can hold, and under 2^29
@@ -159,8 +160,8 @@ struct PagedPlace {
     const int64_t t = g / p.hq;
     p.lse[(g - t * p.hq) * static_cast<int64_t>(p.total_q) + t] = l2 * 0.6931471805599453f;
   }
-  // false: the CTA has no rows or no keys (its outputs are then written here); parts
-  // begin at multiples of ALIGN
+  // false: the CTA is left out, has no rows, or no keys (its outputs are then written
+  // here); parts begin at multiples of ALIGN
   template <int D, int RT, int THREADS, int ALIGN = 16>
   __device__ bool find(const PagedParams& p) {
     const int tid = threadIdx.x;
@@ -172,6 +173,7 @@ struct PagedPlace {
     id /= p.row_tiles;
     split = static_cast<int>(id % p.num_splits);
     b = static_cast<int>(id / p.num_splits);
+    if (p.only && p.only[b] == 0) return false;
     c0 = p.cu[b];
     nq = p.cu[b + 1] - c0;
     r0 = tile * RT;

@@ -202,7 +202,7 @@ struct PagedPlan {
   size_t lse_off;      // workspace: partial O, then partial LSE
   // dense
   int64_t key_rows;    // of the packed copies
-  size_t v_off, cu_q_off, cu_k_off, split_off, split_bytes;
+  size_t v_off, cu_q_off, cu_k_off, odd_off, split_off, split_bytes;
   size_t bytes;        // of the workspace
 };
 
@@ -337,7 +337,8 @@ bool paged_plan_dense(const PagedShape& x, int hkv, int sms, int want, double li
   pl->v_off = align256(copy);
   pl->cu_q_off = pl->v_off + align256(copy);
   pl->cu_k_off = pl->cu_q_off + align256((2 * static_cast<size_t>(x.batch) + 1) * 4);
-  pl->split_off = pl->cu_k_off + align256((2 * static_cast<size_t>(x.batch) + 1) * 4);
+  pl->odd_off = pl->cu_k_off + align256((2 * static_cast<size_t>(x.batch) + 1) * 4);
+  pl->split_off = pl->odd_off + align256(static_cast<size_t>(x.batch) * 4);
   pl->split_bytes = splits > 1 ? attn_fwd_split_workspace_size(static_cast<int32_t>(x.total_q),
                                                                static_cast<int32_t>(x.hq), x.d,
                                                                splits)
@@ -382,7 +383,7 @@ attn_status_t launch_gather(const GatherParams& p, cudaStream_t s) {
   const int page = 1 << p.a.page_shift;
   const int64_t pages = (static_cast<int64_t>(p.max_k) + kGatherPad + page - 1) / page;
   attn_paged_gather_kernel<D, FP8>
-      <<<dim3(static_cast<unsigned>(pages), p.batch, 2), kGatherThreads, 0, s>>>(p);
+      <<<dim3(static_cast<unsigned>(pages), p.batch, 3), kGatherThreads, 0, s>>>(p);
   return launched();
 }
 
@@ -653,8 +654,8 @@ extern "C" attn_status_t attn_paged_fwd(
   if ((st = device_ready(&dev)) != ATTN_OK) return st;
   if (total_q == 0 || max_seqlen_q == 0) return ATTN_OK;
   const PagedMask m = paged_mask(causal, window_left, window_right);
-  const PagedPlan pl = paged_plan(cache, batch, total_q, std::min(max_seqlen_q, total_q),
-                                  max_seqlen_k, nheads_q, m.hi_off, m.lo_off, num_splits, dev->sms);
+  PagedPlan pl = paged_plan(cache, batch, total_q, std::min(max_seqlen_q, total_q), max_seqlen_k,
+                            nheads_q, m.hi_off, m.lo_off, num_splits, dev->sms);
   if (pl.bytes > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
                        workspace_bytes < pl.bytes))
     return ATTN_ERR_INVALID_ARG;
@@ -691,6 +692,7 @@ extern "C" attn_status_t attn_paged_fwd(
   p.k_token = static_cast<uint32_t>(cache->k_s_token) * esz;
   p.v_page = static_cast<uint32_t>(cache->v_s_page) * esz;
   p.v_token = static_cast<uint32_t>(cache->v_s_token) * esz;
+  p.only = nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->type == ATTN_CACHE_E4M3;
   if (pl.dense) {
@@ -703,17 +705,28 @@ extern "C" attn_status_t attn_paged_fwd(
     g.v = reinterpret_cast<uint16_t*>(ws + pl.v_off);
     g.cu_q = reinterpret_cast<int32_t*>(ws + pl.cu_q_off);
     g.cu_k = reinterpret_cast<int32_t*>(ws + pl.cu_k_off);
+    g.odd = reinterpret_cast<int32_t*>(ws + pl.odd_off);
+    if (cudaMemsetAsync(g.odd, 0, static_cast<size_t>(batch) * 4, s) != cudaSuccess)
+      return ATTN_ERR_CUDA;
     switch (cache->head_dim) {
       case 64: st = e4m3 ? launch_gather<64, true>(g, s) : launch_gather<64, false>(g, s); break;
       case 128: st = e4m3 ? launch_gather<128, true>(g, s) : launch_gather<128, false>(g, s); break;
       default: st = e4m3 ? launch_gather<256, true>(g, s) : launch_gather<256, false>(g, s);
     }
     if (st != ATTN_OK) return st;
-    return attn_fwd_split(q, g.k, g.v, g.cu_q, g.cu_k, 2 * batch, total_q,
-                          static_cast<int32_t>(pl.key_rows), max_seqlen_q, max_seqlen_k, nheads_q,
-                          cache->nheads_kv, cache->head_dim, scale, causal, window_left,
-                          window_right, softcap, pl.splits, return_lse, out, lse,
-                          ws + pl.split_off, pl.split_bytes, stream);
+    st = attn_fwd_split(q, g.k, g.v, g.cu_q, g.cu_k, 2 * batch, total_q,
+                        static_cast<int32_t>(pl.key_rows), max_seqlen_q, max_seqlen_k, nheads_q,
+                        cache->nheads_kv, cache->head_dim, scale, causal, window_left,
+                        window_right, softcap, pl.splits, return_lse, out, lse,
+                        ws + pl.split_off, pl.split_bytes, stream);
+    if (st != ATTN_OK) return st;
+    // the sequences that the copies do not serve, over their pages
+    p.only = g.odd;
+    pl.rt = 128;
+    p.num_splits = 1;
+    p.chunk = max_seqlen_k;
+    const int64_t rows = static_cast<int64_t>(p.group) * std::min(max_seqlen_q, total_q);
+    p.row_tiles = static_cast<int>((rows + pl.rt - 1) / pl.rt);
   }
   switch (cache->head_dim) {
     case 64:

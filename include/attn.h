@@ -416,7 +416,10 @@ attn_status_t attn_paged_append(const attn_paged_cache_t* cache, const void* k, 
  * rows of a group or more).  With an e4m3 cache and 17 to 128 rows of a group,
  * elements of q below 2^-10 of their row's largest are held to 2^-17 of it.
  * What the slots of a page past the sequence's length hold, and the pages of
- * other sequences, NaN included, never reaches the result.
+ * other sequences, NaN included, never reaches the result.  A key or value that
+ * is not finite reaches the rows that see it and no others, in every kernel: a
+ * key its rows' O and LSE as NaN, a value its column of them as an infinity or
+ * NaN.  A row of q that is not finite gives NaN for itself alone.
  */
 attn_status_t attn_paged_fwd(const attn_paged_cache_t* cache, const void* q,
                              const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int32_t batch,

@@ -54,7 +54,8 @@ def run(c, q, n, *, hq, splits=0, max_k=None, packed=True, cu=None, **mask):
     need = ea.paged_workspace_size(kc, vc, table, len(n), q.shape[0], max(n), max_k, hq,
                                    num_splits=splits, **where, **kw)
     name, parts = way(need, c, q, len(n), max_k, hq)
-    assert name == ("packed" if packed else "pages") and (splits == 0 or parts == splits)
+    assert name == ("packed" if packed else "pages")
+    assert splits == 0 or parts == splits or (not packed and parts <= splits)
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
     obuf, out, og = guarded_empty(q.shape, BF, kc.device)
     lbuf, lse, lg = guarded_empty((hq, q.shape[0]), torch.float32, kc.device)
@@ -146,6 +147,66 @@ def test_pages_outside_the_pool(pack, d, page, e4m3):
     for splits in (0, 2):
         out, lse = run(c, q, n, hq=4, splits=splits, causal=True)
         compare(out, lse, ref, ref_lse, pabs, False)
+
+
+# (rows, parts) and the way: 65 to 128 rows and more over the pages, and the copies
+ODD = [(65, 1, "0"), (128, 3, "0"), (140, 1, "0"), (65, 0, "1"), (140, 0, "1"), (140, 3, "1")]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("most,splits,way_to", ODD)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_not_finite_values_behind_the_mask(monkeypatch, d, e4m3, most, splits, way_to, bad):
+    """A value that is not finite reaches the rows that see its key and no other row."""
+    if e4m3 and bad == math.inf:
+        return  # e4m3 has no infinity
+    monkeypatch.setenv("ATTN_PAGED_PACK", way_to)
+    page, n, lens = 32, [most, 70, 1, 40], [most + 200, 90, 17, 300]
+    c = Cache(lens, lens, 2, d, page, e4m3, seed=21, junk=math.nan)
+
+    def put(seq, pos, head, col):
+        c.v[int(c.table[seq, pos // page]), pos % page, head, col] = bad
+
+    put(0, lens[0] - 2, 1, 3)     # seen by the last two rows
+    put(0, lens[0] - 1, 0, d - 1)  # by the last only
+    put(0, 240, 1, 9)             # by the rows from 40 on, under no window
+    put(1, 10, 0, 7)              # under the window: by the first rows only
+    q = rows(sum(n), 2, d, 120, 0.2)
+    for args in (dict(causal=True), dict(causal=True, window=(28, -1))):
+        out, lse = run(c, q, n, hq=2, splits=splits, packed=way_to == "1", **args)
+        ref, ref_lse, pabs = sr.attend(q, c.k, c.v, c.k_scale, c.v_scale, c.table, cu_of(n), lens,
+                                       d ** -0.5, **args)
+        got = out.cpu().double()
+        assert torch.equal(~torch.isfinite(got), ref.isnan())
+        compare(torch.where(ref.isnan(), ref, got), lse, ref, ref_lse, pabs, False)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("most,splits,way_to", [(1, 1, "0"), (1, 3, "0"), (5, 2, "0"),
+                                                (20, 1, "0")] + ODD)
+def test_not_finite_keys_and_queries(monkeypatch, d, e4m3, most, splits, way_to):
+    """A key that is not finite makes O and the LSE of the rows that see it NaN, a query
+    its own; with the keys in parts too, where only one of them has it."""
+    monkeypatch.setenv("ATTN_PAGED_PACK", way_to)
+    page, n, lens = 32, [most, most, 1], [most + 200, most + 90, 400]
+    c = Cache(lens, lens, 2, d, page, e4m3, seed=22, junk=math.nan)
+    q = rows(sum(n), 4, d, 121, 0.2)
+    ref, ref_lse, pabs = sr.attend(q, c.k, c.v, c.k_scale, c.v_scale, c.table, cu_of(n), lens,
+                                   d ** -0.5, causal=True)
+    # a key of the last position, seen by the last row; and one seen by every row
+    for seq, pos, seen in ((0, lens[0] - 1, slice(most - 1, most)), (1, 3, slice(most, 2 * most))):
+        c.k[int(c.table[seq, pos // page]), pos % page, seq, 5] = math.nan
+        heads = slice(2 * seq, 2 * seq + 2)  # those of key/value head seq
+        ref[seen, heads] = pabs[seen, heads] = math.nan
+        ref_lse[heads, seen] = math.nan
+    q[2 * most, 1, 7] = math.nan  # the single row of the third sequence, one head
+    ref[2 * most, 1] = pabs[2 * most, 1] = math.nan
+    ref_lse[1, 2 * most] = math.nan
+    out, lse = run(c, q, n, hq=4, splits=splits, packed=way_to == "1", causal=True)
+    assert torch.equal(lse.cpu().isnan(), ref_lse.isnan())
+    compare(out, lse, ref, ref_lse, pabs, False)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
