@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(128, PagedCfg<D, FP8, NT>::CTAS)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              s[kt][nt][x] = pg_cap(s[kt][nt][x] * (rf[nt][x & 1] * sc[kt].ks) * p.cap_mul,
+              s[kt][nt][x] = pg_cap(s[kt][nt][x] * (rf[nt][x & 1] * sc[kt].ks), p.cap_mul,
                                     p.cap_log2);
         }
         if (k0 < w.in_lo || k0 + 16 > w.in_hi || k0 + 16 > ke) {  // some row does not see some key

@@ -15,6 +15,7 @@
 #include <cstdint>
 
 #include "paged_append.cuh"
+#include "ptx.cuh"
 
 namespace attn {
 
@@ -129,9 +130,23 @@ __device__ __forceinline__ uint32_t pg_f16_pair(float lo, float hi) {
   return r;
 }
 
-// c log2(e) tanh(x), x given as 2 log2(e) x: 1 - 2 / (1 + e^2x)
-__device__ __forceinline__ float pg_cap(float x2, float cap_log2) {
-  return cap_log2 * (1.f - __fdividef(2.f, 1.f + pg_ex2(x2)));
+// Softcap c of a score x, both in log2 units: c log2(e) tanh(y) with y = x / (c log2(e)).
+// For |y| <= 1/2 it is x times the polynomial of tanh(y) / y (ptx.cuh), off by some 2^-23 of
+// x however large c is; above that the identity tanh(y) = 1 - 2 / (1 + e^2y), whose error
+// is absolute, some 2^-23 of c, and so of a score that is not far below c.
+constexpr float kCapY = 0.34657359f;  // y = (2 / c) x kCapY: ln(2) / 2
+__device__ __forceinline__ float pg_cap_ratio(float y) {  // tanh(y) / y
+  const float u = y * y;
+  float r = __fmaf_rn(tanhpoly::kA4, u, tanhpoly::kA3);
+  r = __fmaf_rn(r, u, tanhpoly::kA2);
+  r = __fmaf_rn(r, u, tanhpoly::kA1);
+  return __fmaf_rn(r, u, tanhpoly::kA0);
+}
+__device__ __forceinline__ float pg_cap(float x, float cap_mul, float cap_log2) {
+  const float x2 = x * cap_mul, y = x2 * kCapY;
+  return fabsf(y) <= tanhpoly::kY0
+             ? x * pg_cap_ratio(y)
+             : cap_log2 * (1.f - __fdividef(2.f, 1.f + pg_ex2(x2)));
 }
 
 // a CTA's part of the problem

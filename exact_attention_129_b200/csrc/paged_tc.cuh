@@ -383,18 +383,48 @@ __global__ void __launch_bounds__(320, 1)
       const bool edge = mixed(t) || kb + t * BK + BK > ke;
       // (the common case runs without a branch between the blocks, so that their
       // instructions overlap: a warp has its scheduler almost to itself)
-      if (capped || edge) {
+      if (capped) {
+        // where no score of the warp is large, all by the polynomial, in pairs
+        float big = 0.f;
 #pragma unroll
         for (int g = 0; g < NC / 16; ++g) {
           const float f = factor(g);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float x = __uint_as_float(sr[16 * g + i]);
-            if (capped) x = pg_cap(x * f * p.cap_mul, p.cap_log2);
-            const int key = key0 + 16 * g + i;
-            if (key < lo || key > hi) x = -INFINITY;
+            const float x = __uint_as_float(sr[16 * g + i]) * f;
+            big = fmaxf(big, fabsf(x));
             sr[16 * g + i] = __float_as_uint(x);
           }
+        }
+        const float ky = p.cap_mul * kCapY;
+        if (__all_sync(0xffffffffu, big * ky <= tanhpoly::kY0)) {
+          const uint64_t k2 = f2_pack(ky, ky);
+#pragma unroll
+          for (int i = 0; i < NC; i += 2) {
+            const uint64_t x2 =
+                f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+            const uint64_t y2 = f2_mul(x2, k2), u2 = f2_mul(y2, y2);
+            auto both = [](float a) { return f2_pack(a, a); };
+            uint64_t r = f2_fma(both(tanhpoly::kA4), u2, both(tanhpoly::kA3));
+            r = f2_fma(r, u2, both(tanhpoly::kA2));
+            r = f2_fma(r, u2, both(tanhpoly::kA1));
+            r = f2_fma(r, u2, both(tanhpoly::kA0));
+            float a, b;
+            f2_unpack(f2_mul(x2, r), a, b);
+            sr[i] = __float_as_uint(a);
+            sr[i + 1] = __float_as_uint(b);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+            sr[i] = __float_as_uint(pg_cap(__uint_as_float(sr[i]), p.cap_mul, p.cap_log2));
+        }
+      }
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int key = key0 + i;
+          if (key < lo || key > hi) sr[i] = __float_as_uint(-INFINITY);
         }
       }
       float top = -INFINITY;

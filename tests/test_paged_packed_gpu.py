@@ -149,6 +149,22 @@ def test_pages_outside_the_pool(pack, d, page, e4m3):
         compare(out, lse, ref, ref_lse, pabs, False)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("most,way_to", [(1, "0"), (5, "0"), (16, "0"), (60, "0"), (140, "0")])
+@pytest.mark.parametrize("cap", [1e4, 1e6, 1e30])
+def test_large_softcaps(monkeypatch, d, e4m3, most, way_to, cap):
+    # far above the scores the cap changes them by less than rounding, and must not
+    # cost their low bits
+    monkeypatch.setenv("ATTN_PAGED_PACK", way_to)
+    n, lens = [most, 1], [most + 200, 70]
+    c = Cache(lens, lens, 2, d, 64, e4m3, seed=19, junk=math.nan)
+    q = rows(sum(n), 4, d, 525, 0.2)
+    for mask in (dict(causal=True), dict(window=(90, 10))):
+        check(c, q, n, hq=4, packed=way_to == "1", softcap=cap, f16=e4m3 and way_to == "0",
+              splits=2, **mask)
+
+
 # (rows, parts) and the way: 65 to 128 rows and more over the pages, and the copies
 ODD = [(65, 1, "0"), (128, 3, "0"), (140, 1, "0"), (65, 0, "1"), (140, 0, "1"), (140, 3, "1")]
 
