@@ -120,24 +120,30 @@ __device__ __forceinline__ uint32_t fwd_cap(const FwdParams& p, uint32_t bits) {
   return x == -INFINITY ? bits : __float_as_uint(p.cap_log2 * tanh_from_ex2(x * p.cap_k2));
 }
 
-// softcap of a thread's scores in place, in the log2 domain.  When no score of
-// the block is masked and every score of the warp has |s scale / c| <= 1/2,
-// tanh runs as an odd polynomial on the FMA pipe (softcap_poly_pair);
-// otherwise every score takes the identity through ex2 and rcp (fwd_cap;
-// masked -inf stays -inf).  `masked` is the same for the whole warp.
+// softcap of a thread's scores in place, in the log2 domain.  When every score
+// of the warp that is not masked has |s scale / c| <= 1/2, tanh runs as an odd
+// polynomial on the FMA pipe (softcap_poly_pair), whose error is relative, so
+// that a large c costs no bits; otherwise every score takes the identity through
+// ex2 and rcp (fwd_cap), whose error is some 2^-23 of c.  Masked scores (-inf)
+// stay -inf both ways (the polynomial's last coefficient is positive).
+// `masked`, the same for the whole warp: the block has some.
 template <int N>
 __device__ __forceinline__ void fwd_cap_scores(const FwdParams& p, uint32_t (&sr)[N],
                                                bool masked) {
   static_assert(N % 2 == 0, "score pairs");
-  bool poly = false;
-  if (!masked) {
-    float ma = 0.f;
+  float ma = 0.f;
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = __uint_as_float(sr[i]);
+      ma = fmaxf(ma, x == -INFINITY ? 0.f : fabsf(x));
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < N; i += 2)
       ma = fmax3(ma, fabsf(__uint_as_float(sr[i])), fabsf(__uint_as_float(sr[i + 1])));
-    poly = __all_sync(0xffffffffu, ma * p.cap_k1 <= tanhpoly::kY0);
   }
-  if (poly) {
+  if (__all_sync(0xffffffffu, ma * p.cap_k1 <= tanhpoly::kY0)) {
     const float K = p.cap_log2;
     const uint64_t k1 = f2_pack(p.cap_k1, p.cap_k1);
     const uint64_t ka[5] = {f2_pack(K * tanhpoly::kA0, K * tanhpoly::kA0),

@@ -151,7 +151,8 @@ def test_pages_outside_the_pool(pack, d, page, e4m3):
 
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("e4m3", [False, True])
-@pytest.mark.parametrize("most,way_to", [(1, "0"), (5, "0"), (16, "0"), (60, "0"), (140, "0")])
+@pytest.mark.parametrize("most,way_to", [(1, "0"), (5, "0"), (16, "0"), (60, "0"), (140, "0"),
+                                         (140, "1")])
 @pytest.mark.parametrize("cap", [1e4, 1e6, 1e30])
 def test_large_softcaps(monkeypatch, d, e4m3, most, way_to, cap):
     # far above the scores the cap changes them by less than rounding, and must not
