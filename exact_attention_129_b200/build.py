@@ -1,5 +1,5 @@
 """Ahead-of-time build of libattn.so (sm_100a, nvcc) and of the compiled part of
-its Python binding, _serving.so (g++), in the source tree.
+its Python binding, _serving.*.so (g++), in the source tree.
 
 Usage: python -m exact_attention_129_b200.build [--force] [--debug]
 """
@@ -20,7 +20,6 @@ HEADERS = ["ptx.cuh", "fwd_kernel.cuh", "fwd_pair_kernel.cuh", "bwd_kernels.cuh"
            "bwd_pair_kernel.cuh", "rotary.cuh", "paged_append.cuh", "paged_common.cuh",
            "paged_attn.cuh",
            "paged_gather.cuh", "paged_tc.cuh"]
-BINDING = os.path.join(HERE, "_serving.so")
 BINDING_SOURCE = os.path.join(CSRC, "serving_binding.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -63,18 +62,20 @@ def build(force: bool = False, verbose: bool = False, extra=(), out: str | None 
 
 
 def build_binding(force: bool = False) -> str:
-    """Compile _serving.so against the installed torch; it calls libattn.so through
-    addresses it is given, so it does not link to it."""
+    """Compile the binding against the installed torch, under a name that carries its
+    version; it calls libattn.so through addresses it is given, so it does not link to it."""
+    from exact_attention_129_b200.serving import binding_path
+    target = binding_path()
     inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "attn.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(BINDING) and \
-            all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
-        return BINDING
+    if not force and os.path.exists(target) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(target) for f in inputs):
+        return target
     import sysconfig
 
     import torch
     base = os.path.join(os.path.dirname(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(NVCC))
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = target + f".tmp{os.getpid()}"
     includes = [INCLUDE, os.path.join(base, "include"),
                 os.path.join(base, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
@@ -85,9 +86,9 @@ def build_binding(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("g++ failed building _serving.so")
-    os.replace(tmp, BINDING)
-    return BINDING
+        raise RuntimeError(f"g++ failed building {os.path.basename(target)}")
+    os.replace(tmp, target)
+    return target
 
 
 if __name__ == "__main__":

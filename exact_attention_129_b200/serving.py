@@ -29,19 +29,26 @@ __all__ = ["rope_frequencies", "attn_rotary", "rotary", "attn_paged_append", "at
 
 _ea = sys.modules[__package__]  # the package's loader, looked up when it is needed
 
-BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_serving.so")
 ABI = ("attn_rotary", "attn_paged_append", "attn_paged_fwd", "attn_paged_workspace_size")
 _binding = None
+
+
+def binding_path() -> str:
+    """The compiled binding for the running Python and torch.  It is built against their
+    C++ headers, so another version of either has another file and never loads this one."""
+    tag = f"{sys.implementation.cache_tag}-torch{torch.__version__}"
+    return os.path.join(os.path.dirname(os.path.abspath(__file__)), f"_serving.{tag}.so")
 
 
 def _load():
     """The compiled binding, bound to the loaded libattn.so."""
     global _binding
-    if not os.path.exists(BINDING_PATH):
-        raise ImportError(f"{BINDING_PATH} is missing: build it with `python -m "
+    path = binding_path()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python -m "
                           "exact_attention_129_b200.build`")
     lib = _ea.library()
-    spec = importlib.util.spec_from_file_location(f"{__package__}._serving", BINDING_PATH)
+    spec = importlib.util.spec_from_file_location(f"{__package__}._serving", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     module.init(_ea.AttnError,
