@@ -232,7 +232,7 @@ struct PagedShape {
 
 constexpr double kRoundNs[2] = {3000.0, 6000.0};  // a CTA's set-up and drain: mma.sync, tcgen05
 constexpr double kEqualBatches = 0.45;
-constexpr double kSpread[2] = {0.2, 0.0};  // of a CTA's time: three on an SM, or one
+constexpr double kSpread[2] = {0.2, 0.0};  // of a CTA's time: mma.sync kernel, tcgen05 kernel
 constexpr double kMergeCopies = 2.0;  // the parts of O cross HBM or L2 about so often
 
 // one round of k CTAs of chunk keys side by side
@@ -284,8 +284,10 @@ double paged_plan_tiles(const PagedShape& x, int want, int sms, PagedPlan* pl) {
           (1. - kEqualBatches) * ragged_ns(0.6 * n, slots, c, key, x.key_bytes, fixed);
     // CTAs side by side do not end together: 16 sequences of 64K take 334 us with one
     // long CTA per slot when all goes well, 356 to 390 in most runs, with 16 parts 333 to
-    // 375.  (The tcgen05 kernel, alone on its SM, does not gain: drafts 74 us without
-    // this term, 88 with 0.2.)
+    // 375.  The same holds where one CTA of the mma.sync kernel fills an SM (bf16 with
+    // head_dim 256): 128 sequences of 16K 814 us with the parts this term leads to, 868
+    // without, 3 of 64K 315 and 341, though 16 of 1000 keys 37 and 32.  (The tcgen05
+    // kernel does not gain: drafts 74 us without this term, 88 with 0.2.)
     t += 4000. + kSpread[ri > 1] * round_ns(std::min(n, slots), c, key, x.key_bytes, 0.);
     if (parts > 1)
       t += 2000. + kMergeCopies * 8. * parts * x.total_q * x.hq * x.d / kHbmBytesPerNs;

@@ -208,3 +208,40 @@ def test_gradient_in_a_graph():
     assert all(torch.equal(-a, b) for a, b in zip(want, got))
     again = torch.autograd.grad(ea.rotary(q, k, f), (q, k), g)
     assert all(torch.equal(a, b) for a, b in zip(again, got))
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("both", [False, True])
+def test_gradient_of_the_gradient(inter, both):
+    # y = R x, so dx(w) = R^T w, which is linear in w: the gradient of <dx(w), u> by w is R u,
+    # the gradient of <dx(w(x)), u> by x goes on through w(x), and a third one turns back again
+    t, d = 21, 128
+    f, m = ea.rope_frequencies(d, scaling="yarn", factor=4, original_max=4096)
+    f, cu = f.cuda(), torch.tensor([0, 9, 21], dtype=torch.int32).cuda()
+    how = dict(cu_seqlens=cu, interleaved=inter, mscale=m)
+    heads = (4, 2) if both else (4,)
+    x, w, u, z = ([rows(t, h, d, s + h).cuda() for h in heads] for s in (50, 60, 70, 80))
+    for part in (x, w, u):
+        for i in part:
+            i.requires_grad_(True)
+
+    def turn(p, inverse):
+        out = ea.attn_rotary(p[0].detach(), p[1].detach() if both else None, f, inverse=inverse,
+                             **how)
+        return out if both else out[:1]
+
+    y = ea.rotary(x[0], x[1] if both else None, f, **how)[:len(heads)]
+    dx = torch.autograd.grad(y, x, w, create_graph=True)
+    assert all(i.requires_grad for i in dx)
+    for got, want in zip(dx, turn(w, True)):
+        assert torch.equal(got, want)
+    ddw = torch.autograd.grad(dx, w, u, create_graph=True)
+    for got, want in zip(ddw, turn(u, False)):
+        assert torch.equal(got, want)
+    for got, want in zip(torch.autograd.grad(ddw, u, z), turn(z, True)):
+        assert torch.equal(got, want)
+    # through w(x) = x: d/dx <R^T x, u> = R u
+    y = ea.rotary(x[0], x[1] if both else None, f, **how)[:len(heads)]
+    dx = torch.autograd.grad(y, x, x, create_graph=True)
+    for got, want in zip(torch.autograd.grad(dx, x, [i.detach() for i in u]), turn(u, False)):
+        assert torch.equal(got, want)
