@@ -413,7 +413,8 @@ attn_status_t attn_paged_append(const attn_paged_cache_t* cache, const void* k, 
  *                  other num_splits needs the parts of O alone.
  * Scores and sums are fp32.  The weights are rounded to bf16 for the product with
  * the values (f16 with an e4m3 cache, bf16 where its keys are packed first: 128
- * rows of a group or more).  With an e4m3 cache and 17 to 128 rows of a group,
+ * rows of a group or more; there keys and values under scales that are no powers
+ * of two are rounded to bf16 as well).  With an e4m3 cache and 17 to 128 rows of a group,
  * elements of q below 2^-10 of their row's largest are held to 2^-17 of it.
  * What the slots of a page past the sequence's length hold, and the pages of
  * other sequences, NaN included, never reaches the result.  A key or value that
