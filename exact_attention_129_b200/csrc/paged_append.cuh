@@ -76,8 +76,11 @@ __device__ __forceinline__ PageSpan page_span(const AppendParams& p, int b, int 
   const int start = len - n;
   const int jp = (start >> p.page_shift) + j;  // below 0 for positions below 0
   s.row0 = static_cast<int64_t>(c0) - start;
-  s.first = max(start, jp << p.page_shift);
-  s.last = min(len, (jp + 1) << p.page_shift);
+  // (a page may begin or end past 32 bits)
+  const int64_t begin = static_cast<int64_t>(jp) << p.page_shift;
+  const int64_t end = begin + (int64_t(1) << p.page_shift);
+  s.first = begin >= len ? len : max(start, static_cast<int>(begin));
+  s.last = end < len ? static_cast<int>(end) : len;
   s.page = -1;
   if (n > 0 && s.first < s.last && jp >= 0 && jp < p.pages_per_seq) {
     const int page = p.table[b * p.table_stride + jp];

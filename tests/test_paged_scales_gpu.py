@@ -80,3 +80,25 @@ def test_attention_through_packed_copies(monkeypatch, d, splits):
     out, lse = ea.attn_paged_fwd(q.cuda(), kc, vc, table, i32(cu_of(n)), i32(lens), max(n), 400,
                                  causal=True, num_splits=splits, **kw)
     compare(out, lse, *ref, False)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n", [3, 20])
+def test_append_at_the_last_positions(e4m3, n):
+    # positions up to 2^31 - 2 lie past any block table: nothing is written, and the
+    # queries are rotated by them all the same, in both kernels
+    d, page, top = 64, 16, 2 ** 31 - 1
+    c = Cache([16], [16], 2, d, page, e4m3, seed=94)
+    k, q = rows(n, 2, d, 95).cuda(), rows(n, 4, d, 96).cuda()
+    kc, vc, table, kw = c.to("cuda")
+    f = ea.rope_frequencies(d)[0].cuda()
+    out = ea.attn_paged_append(k, k, kc, vc, table, i32([0, n]), i32([top]), n, q=q, inv_freq=f,
+                               **kw)
+    pos = torch.arange(top - n, top, dtype=torch.int64)
+    want = ea.attn_rotary(q, None, f, positions=pos.int().cuda())[0]
+    assert torch.equal(out, want)
+    # in place: each row is rotated once
+    ea.attn_paged_append(k, k, kc, vc, table, i32([0, n]), i32([top]), n, q=q, q_out=q, inv_freq=f,
+                         **kw)
+    assert torch.equal(q, want)
+    assert same_codes(kc.cpu(), c.k) and same_codes(vc.cpu(), c.v)
