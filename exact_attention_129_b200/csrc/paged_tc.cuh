@@ -260,8 +260,9 @@ __global__ void __launch_bounds__(320, 1)
           reinterpret_cast<const uint4*>(p.q + w.row_index(p, live ? r : 0) * D);
       if constexpr (FP8) {
         // scaled so that the largest element is in [2^7, 2^8), and as a sum of two codes:
-        // 4 significant bits, then the rest; exact for elements down to 2^-10 of that, and
-        // smaller ones are off by at most half the least code, 2^-17 of the largest
+        // 4 significant bits, then the rest; exact for elements down to 2^-2, which are those
+        // down to 2^-9 of the largest, and smaller ones are off by at most half the least
+        // code, 2^-17 of the largest
         uint32_t m = 0;
 #pragma unroll 8
         for (int i = 0; i < D / 8; ++i) {

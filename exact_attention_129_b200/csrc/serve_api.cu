@@ -317,6 +317,7 @@ bool paged_plan_dense(const PagedShape& x, int hkv, int sms, int want, double li
   const int64_t copy = key_rows * hkv * x.d * 2;
   if (x.batch > 32767 || 2 * copy > kDenseBytes || key_rows >= (1 << 30)) return false;
   if (!forced && (x.rows < 128 || x.max_k < 512)) return false;
+  if (x.units * ((x.rows + 127) / 128) > kMaxGrid) return false;  // the launch over the pages
   // code read, copy written and read; three launches more
   const double gather = 16000. + key_rows * hkv * (x.key_bytes + 8. * x.d) / kHbmBytesPerNs;
   const int64_t tile = x.d == 256 ? 128 : 256;

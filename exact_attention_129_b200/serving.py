@@ -67,8 +67,11 @@ def rope_frequencies(rot_dim, base=10000.0, *, scaling=None, factor=1.0, origina
     so that the fastest pair keeps its angle and the slowest is divided by the
     factor); "yarn" (pairs that turn more than ``beta_fast`` times over
     ``original_max`` positions keep their angle, those under ``beta_slow`` turns
-    are divided, a linear ramp between; the factor on the values is
-    0.1 ln(factor) + 1)."""
+    are divided, a ramp between that is linear in the number of turns, as the YaRN
+    paper defines it; the factor on the values is 0.1 ln(factor) + 1).  Some released
+    checkpoints ramp linearly in the pair's index between two rounded bounds instead,
+    which gives other angles in the middle: compute ``inv_freq`` as such a checkpoint
+    does and pass that."""
     rot_dim = int(rot_dim)
     if rot_dim < 16 or rot_dim % 16:
         raise ValueError(f"rot_dim must be a positive multiple of 16, got {rot_dim}")

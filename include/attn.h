@@ -275,8 +275,11 @@ attn_status_t attn_bwd_static_scratch(const void* q, const void* k, const void* 
  *
  * With R = 2 * num_freqs, pair i < num_freqs of a row at position pos is
  * (x[i], x[i + R/2]), or (x[2i], x[2i+1]) when interleaved, and becomes, for
- * theta = pos * inv_freq[i] (computed in 64 bits),
+ * theta = pos * inv_freq[i],
  *   a' = mscale (a cos theta - b sin theta), b' = mscale (b cos theta + a sin theta);
+ * theta is computed in 64 bits and reduced by whole turns there, then rounded to
+ * 32 bits for cosine and sine (off by up to 2e-7), and a' and b' are rounded to
+ * bf16 once;
  * elements from R on are copied.  inverse = 1 turns by -theta: the gradient of
  * the forward rotation with respect to its input, given the output's.
  *
@@ -415,12 +418,12 @@ attn_status_t attn_paged_append(const attn_paged_cache_t* cache, const void* k, 
  * the values (f16 with an e4m3 cache, bf16 where its keys are packed first: 128
  * rows of a group or more; there keys and values under scales that are no powers
  * of two are rounded to bf16 as well).  With an e4m3 cache and 17 to 128 rows of a group,
- * elements of q below 2^-10 of their row's largest are held to 2^-17 of it.
+ * elements of q below 2^-9 of their row's largest are held to 2^-17 of it.
  * What the slots of a page past the sequence's length hold, and the pages of
  * other sequences, NaN included, never reaches the result.  A key or value that
  * is not finite reaches the rows that see it and no others, in every kernel: a
- * key its rows' O and LSE as NaN, a value its column of them as an infinity or
- * NaN.  A row of q that is not finite gives NaN for itself alone.
+ * NaN key makes their O and LSE NaN, a value its column of their O an infinity
+ * or NaN.  A row of q with a NaN gives NaN for itself alone.
  */
 attn_status_t attn_paged_fwd(const attn_paged_cache_t* cache, const void* q,
                              const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int32_t batch,
