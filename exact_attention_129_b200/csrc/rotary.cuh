@@ -8,10 +8,12 @@
 // x[R:] is copied.  The map is orthogonal up to m, so its gradient is the same
 // map with -theta (`sign` = -1).
 //
-// The angle is taken in 64 bits: theta / 2 pi is reduced to [-1/2, 1/2] before
-// it is rounded to fp32, so a position of a million loses nothing (in fp32 the
-// product alone would be off by 2^-4 radians there).  cos and sin are fp32, the
-// pair is computed in fp32 and rounded to bf16 once.
+// The angle, its reduction by quarter turns and its sine and cosine are taken in
+// 64 bits, by Taylor sums on [-pi/4, pi/4], and rounded to fp32 once: a position
+// of a million loses nothing (in fp32 the product alone would be off by 2^-4
+// radians there), and neither do pairs that nearly cancel (an angle rounded to
+// fp32 before its sine turns them by up to 2^-23).  The pair is computed in fp32
+// and rounded to bf16 once.
 //
 // Work unit: 16 elements of a row = 8 pairs = two 16-byte loads and stores.  In
 // the half layout they are x[8c..] and x[R/2 + 8c..], so the lanes of a row
@@ -56,14 +58,29 @@ __device__ __forceinline__ void rope_offsets(const RopeParams& r, int c, int* a,
 __device__ __forceinline__ void rope_angles(const RopeParams& r, int c, int pos, float (&cs)[8],
                                             float (&sn)[8]) {
   const double p = static_cast<double>(pos);
-#pragma unroll
+  constexpr double M = 6755399441055744.0;  // 1.5 2^52: h + M rounds h to a whole number,
+#pragma unroll                              // whose low bits are those of the sum
   for (int i = 0; i < 8; ++i) {
-    const double turns = p * r.inv_freq[8 * c + i] * 0.15915494309189533577;
-    const float x = static_cast<float>(2.0 * (turns - rint(turns)));
-    float s, k;
-    sincospif(x, &s, &k);
-    cs[i] = r.mscale * k;
-    sn[i] = r.mscale * (r.sign * s);
+    const double h = __dmul_rn(__dmul_rn(p, r.inv_freq[8 * c + i]), 0.63661977236758134308);
+    const double t = __dadd_rn(h, M);
+    const int quarter = __double2loint(t) & 3;
+    // the rest, at most half a quarter turn, in radians; cut off below 2^-32 of the results
+    const double z = __dmul_rn(__dsub_rn(h, __dsub_rn(t, M)), 1.57079632679489661923);
+    const double u = __dmul_rn(z, z);
+    double a = __fma_rn(u, -1.0 / 39916800.0, 1.0 / 362880.0);
+    a = __fma_rn(a, u, -1.0 / 5040.0);
+    a = __fma_rn(a, u, 1.0 / 120.0);
+    a = __fma_rn(a, u, -1.0 / 6.0);
+    double b = __fma_rn(u, -1.0 / 3628800.0, 1.0 / 40320.0);
+    b = __fma_rn(b, u, -1.0 / 720.0);
+    b = __fma_rn(b, u, 1.0 / 24.0);
+    b = __fma_rn(b, u, -0.5);
+    const float s = static_cast<float>(__fma_rn(__dmul_rn(z, u), a, z));
+    const float k = static_cast<float>(__fma_rn(u, b, 1.0));
+    // turned by the whole quarters: (k, s), (-s, k), (-k, -s), (s, -k)
+    const float ck = quarter & 1 ? s : k, sk = quarter & 1 ? k : s;
+    cs[i] = r.mscale * ((quarter + 1) & 2 ? -ck : ck);
+    sn[i] = r.mscale * (r.sign * (quarter & 2 ? -sk : sk));
   }
 }
 

@@ -277,9 +277,8 @@ attn_status_t attn_bwd_static_scratch(const void* q, const void* k, const void* 
  * (x[i], x[i + R/2]), or (x[2i], x[2i+1]) when interleaved, and becomes, for
  * theta = pos * inv_freq[i],
  *   a' = mscale (a cos theta - b sin theta), b' = mscale (b cos theta + a sin theta);
- * theta is computed in 64 bits and reduced by whole turns there, then rounded to
- * 32 bits for cosine and sine (off by up to 2e-7), and a' and b' are rounded to
- * bf16 once;
+ * theta, its cosine and its sine are computed in 64 bits; the two are rounded to
+ * 32 bits, a' and b' computed in 32 bits and rounded to bf16 once;
  * elements from R on are copied.  inverse = 1 turns by -theta: the gradient of
  * the forward rotation with respect to its input, given the output's.
  *

@@ -245,3 +245,37 @@ def test_gradient_of_the_gradient(inter, both):
     dx = torch.autograd.grad(y, x, x, create_graph=True)
     for got, want in zip(torch.autograd.grad(dx, x, [i.detach() for i in u]), turn(u, False)):
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("offset", [0, 10 ** 6, -500])
+def test_pairs_that_nearly_cancel(inter, offset):
+    # a cos - b sin is far below a and b: what is left shows the error of cosine and sine,
+    # which are to be the 64-bit ones rounded to fp32 once.  With u = 2^-24, half a step:
+    # |a c| u for the product with a rounded c; 2 |b s| u for b s, rounded itself; u of the
+    # result; and 2^-30 (|a| + |b|) for the sine and cosine before their rounding
+    t, d = 200000, 64
+    f = ea.rope_frequencies(d, 500000.0)[0]
+    x = rows(t, 1, d, 23)
+    out = ea.attn_rotary(x.cuda(), None, f.cuda(), cu_seqlens=torch.tensor([0, t]).int().cuda(),
+                         offsets=torch.tensor([offset]).int().cuda(), interleaved=inter)[0].cpu()
+    ang = (torch.arange(t, dtype=torch.float64) + offset)[:, None] * f[None, :]
+    c, s = ang.cos(), ang.sin()
+
+    def halves(y):
+        y = y[:, 0].double()
+        return (y[:, 0::2], y[:, 1::2]) if inter else (y[:, :d // 2], y[:, d // 2:])
+
+    a, b = halves(x)
+    ga, gb = halves(out)
+    seen = 0
+    for got, p, q in ((ga, a * c, -b * s), (gb, b * c, a * s)):
+        want = p + q
+        u = 2.0 ** -24
+        bound = u * (p.abs() + 2 * q.abs() + want.abs()) + 2.0 ** -30 * (a.abs() + b.abs())
+        close = want.abs() < 2.0 ** -12
+        seen += int(close.sum())
+        err = (got - want).abs()
+        assert bool((err <= bound + sr.U_BF16 * (want.abs() + bound))[close].all()), float(
+            (err / bound)[close].max())
+    assert seen > 1000
