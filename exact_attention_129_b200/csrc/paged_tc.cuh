@@ -34,8 +34,9 @@
 // 16 MMAs of 64 keys for S take about 50 cycles each, a full-rate one would take 16; with
 // P V they fill 1400 of the 1500.)  P V from a warp of its own, or the zero weights
 // written before the softmax, changed nothing.  One CTA alone, 32
-// rows, e4m3: 7.6, 9.2 and 17 ns a key of head_dim 64, 128, 256; bf16 6.0, 7.7, 14.2,
-// where 512 CTAs run at 4.4, 5.8 and 6.2 TB/s.  More CTAs an SM (smaller tiles, one slot
+// rows, 128K keys, e4m3: 5.7, 6.7 and 12.5 ns a key of head_dim 64, 128, 256; bf16 4.3,
+// 5.9, 13.5; 148 of them with 4096 keys each, launch and drain included, 8.6, 11.2, 20.4
+// and 8.9, 13.3, 24.2 (bf16 of head_dim 256: 6.3 TB/s).  More CTAs an SM (smaller tiles, one slot
 // of S) gave 41 ns a key of 512 CTAs of e4m3 and head_dim 128, one CTA with these 38.
 //
 // The weights, m and l are as in paged_attn.cuh.  Every wait is bounded.

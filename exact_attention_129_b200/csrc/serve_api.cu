@@ -215,7 +215,10 @@ constexpr int64_t kDenseBytes = int64_t(4) << 30;  // the packed copies may take
 // tcgen05 kernel.  512 CTAs of 16 rows of head_dim 64, 128, 256: e4m3 24, 32, 61 ns a key
 // in the mma.sync kernel, 29, 36, 67 in the other; bf16 29, 46, 120 and 29, 44, 82.
 constexpr int kPagedRows[5] = {8, 16, 32, 64, 128};
-// ns per key of one CTA, by type, head_dim and rows, where HBM does not set the pace
+// ns per key of one CTA, by type, head_dim and rows, where HBM does not set the pace.
+// (Between what a CTA takes alone over 128K keys and what it takes in a full round of
+// 4096: e4m3, head_dim 128, 8 / 16 / 32 / 64 / 128 rows 9.3 / 11.2 / 6.7 / 9.1 / 15.1 and
+// 18.4 / 16.7 / 11.2 / 13.7 / 20.9.)
 constexpr double kPagedNsPerKey[2][3][5] = {{{9., 0., 6., 7., 11.},
                                              {15., 0., 7.7, 8.2, 12.},
                                              {23., 0., 14.2, 15., 16.2}},
