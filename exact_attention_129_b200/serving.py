@@ -113,8 +113,9 @@ def rotary(q, k, inv_freq, *, cu_seqlens=None, offsets=None, positions=None, int
            mscale=1.0):
     """Differentiable attn_rotary: the gradient, of q and k, is the inverse rotation.
 
-    A backward can be captured into a CUDA graph when no eager graph of the same
-    leaves is alive (torch refuses the capture otherwise)."""
+    A backward can be captured into a CUDA graph only when no eager graph of the same
+    leaves is alive: torch refuses the capture otherwise, which can end the process, so
+    drop the outputs of eager calls first."""
     return (_binding or _load()).rotary_grad(q, k, inv_freq, cu_seqlens, offsets, positions,
                                              interleaved, mscale)
 

@@ -98,6 +98,17 @@ def test_values(pack, d, e4m3, mask):
             check(c, q, n, hq=hq, splits=splits, **mask)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("splits", [0, 2])
+def test_sequences_without_keys(pack, e4m3, splits):
+    # every row sees nothing: max_seqlen_k 0, and an empty block table
+    c = Cache([0, 0], [0, 0], 2, 128, 64, e4m3, seed=16)
+    q = rows(130, 4, 128, 505, 0.2)
+    for max_k in (0, 300):
+        out, lse = check(c, q, [100, 30], hq=4, splits=splits, max_k=max_k, causal=True)
+        assert not out.any() and bool((lse == -math.inf).all())
+
+
 @pytest.mark.parametrize("d,e4m3,n,lens,hq,hkv,parts", [
     (128, True, [500, 100], [3000, 2100], 8, 2, 4), (64, True, [500, 100], [3000, 2100], 8, 2, 4),
     (64, False, [500, 100, 500, 500], [2000, 600, 500, 1500], 16, 4, 1)])
