@@ -386,7 +386,9 @@ __global__ void __launch_bounds__(320, 1)
       // (the common case runs without a branch between the blocks, so that their
       // instructions overlap: a warp has its scheduler almost to itself)
       if (capped) {
-        // where no score of the warp is large, all by the polynomial, in pairs
+        // where no score of the warp is large, all by the polynomial, in pairs (not in
+        // tiles with keys that are not seen: among those are some that were not loaded,
+        // and what their memory happens to hold must not decide)
         float big = 0.f;
 #pragma unroll
         for (int g = 0; g < NC / 16; ++g) {
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(320, 1)
           }
         }
         const float ky = p.cap_mul * kCapY;
-        if (__all_sync(0xffffffffu, big * ky <= tanhpoly::kY0)) {
+        if (!edge && __all_sync(0xffffffffu, big * ky <= tanhpoly::kY0)) {
           const uint64_t k2 = f2_pack(ky, ky);
 #pragma unroll
           for (int i = 0; i < NC; i += 2) {

@@ -177,6 +177,38 @@ def test_large_softcaps(monkeypatch, d, e4m3, most, way_to, cap):
               splits=2, **mask)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,way_to", [(1, "0"), (5, "0"), (12, "0"), (40, "0"), (130, "0"),
+                                      (130, "1")])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_the_same_bits_whatever_ran_before(monkeypatch, d, e4m3, n, way_to, cap):
+    # a call's last tile is partly loaded: what an earlier call left in shared memory, large
+    # keys here, must not decide how its scores are computed
+    monkeypatch.setenv("ATTN_PAGED_PACK", way_to)
+    seqs, size = 148, 228  # every SM, and 100 keys of a second tile
+    c = Cache([size] * 4, [256] * 4, 1, d, 16, e4m3, seed=20)
+    kc, vc, table, kw = c.to("cuda")
+    table = table.repeat(seqs // 4, 1)
+    big = torch.full_like(kc.float(), 448.0)
+    big[:, ::2] = -448.0
+    big = big.to(kc.dtype)
+    q = rows(seqs * n, 1, d, 560, 0.0).cuda()
+    cu = i32([n * i for i in range(seqs + 1)])
+
+    def call(keys, length):
+        return ea.attn_paged_fwd(q, keys, vc, table, cu, i32([length] * seqs), n, 256, causal=True,
+                                 window=(200, 0), softcap=cap, num_splits=1, **kw)
+
+    got = []
+    for before in (torch.zeros_like(kc.float()).to(kc.dtype), big, kc):
+        call(before, 256)
+        got.append(call(kc, size))
+    assert bool(torch.isfinite(got[0][0]).all())
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
 # (rows, parts) and the way: 65 to 128 rows and more over the pages, and the copies
 ODD = [(65, 1, "0"), (128, 3, "0"), (140, 1, "0"), (65, 0, "1"), (140, 0, "1"), (140, 3, "1")]
 
