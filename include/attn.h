@@ -414,8 +414,9 @@ attn_status_t attn_paged_append(const attn_paged_cache_t* cache, const void* k, 
  *                  may hold bf16 copies of all keys and values, up to 4 GiB; any
  *                  other num_splits needs the parts of O alone.
  * Scores and sums are fp32.  The weights are rounded to bf16 for the product with
- * the values (f16 with an e4m3 cache, bf16 where its keys are packed first: 128
- * rows of a group or more; there keys and values under scales that are no powers
+ * the values (f16 with an e4m3 cache, where weights times their page's value scale
+ * below 2^-20 of the row's largest lose bits and go in steps of 2^-30 of it; bf16
+ * where its keys are packed first: 128 rows of a group or more; there keys and values under scales that are no powers
  * of two are rounded to bf16 as well).  With an e4m3 cache and 17 to 128 rows of a group,
  * elements of q below 2^-9 of their row's largest are held to 2^-17 of it.
  * What the slots of a page past the sequence's length hold, and the pages of
